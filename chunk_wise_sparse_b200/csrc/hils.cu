@@ -19,6 +19,8 @@
 #include "qcal.cuh"
 #include "backward.cuh"
 #include "backward_mma.cuh"
+#include "append.cuh"
+#include "decode_quant.cuh"
 
 using namespace hils;
 
@@ -819,6 +821,276 @@ int hils_query_calibrate(const hils_dims* d, const void* q, int64_t n_pos, const
     else qcal_simt_kernel<float, 128><<<blocks, 128, 0, st>>>(qq, wd, wu, rank, n_pos, d->heads_q, rows, out);
   }
   return launched(1);
+}
+
+// ---------------------------------------------------------------- chunk-paged serving
+// The ragged batch of an append, read-back or summary: HILS_OK with
+// n_tokens == 0 means nothing to do.
+static int check_tokens(const hils_dims* d, const hils_tokens* tk, TokenBatch* tb) {
+  const int rc = check_dims(d);
+  if (rc) return rc;
+  if (tk == nullptr || tk->n_tokens < 0) return HILS_ERR_INVALID_ARGUMENT;
+  if (tk->cu_tokens == nullptr && tk->n_tokens % d->batch != 0) return HILS_ERR_INVALID_ARGUMENT;
+  if (tk->n_tokens >= (int64_t(1) << 31)) return HILS_ERR_UNSUPPORTED;
+  if (tk->n_tokens > 0 && (!ptr_ok(tk->seqlens) || !aligned16(tk->cu_tokens))) return HILS_ERR_INVALID_ARGUMENT;
+  tb->cu = tk->cu_tokens;
+  tb->seqlens = tk->seqlens;
+  tb->n_tokens = tk->n_tokens;
+  tb->per = tk->cu_tokens == nullptr ? tk->n_tokens / d->batch : 0;
+  tb->cap = d->seqlen;
+  tb->batch = d->batch;
+  return HILS_OK;
+}
+
+// Rows [T, heads, d]: 16-byte aligned, strides in elements of whole 16-byte
+// pieces; those of an output must not make two rows overlap.
+static bool rows_ok(const hils_rows* r, const hils_dims* d, int64_t T, int64_t heads, bool output) {
+  if (r == nullptr || !ptr_ok(r->data)) return false;
+  const int64_t per16 = d->dtype == HILS_BF16 ? 8 : 4, D = d->head_dim, ts = r->token_stride, hs = r->head_stride;
+  if (ts < 0 || hs < 0 || ts % per16 != 0 || hs % per16 != 0) return false;
+  if (ts > (int64_t(1) << 40) || hs > (int64_t(1) << 40)) return false;
+  if (!output) return true;
+  if ((T > 1 && ts < D) || (heads > 1 && hs < D)) return false;
+  return T == 1 || heads == 1 || ts >= (heads - 1) * hs + D || hs >= (T - 1) * ts + D;
+}
+static RowsView rows_view(const hils_rows* r) {
+  return r == nullptr ? RowsView{nullptr, 0, 0} : RowsView{r->data, r->token_stride, r->head_stride};
+}
+
+}  // extern "C"
+
+namespace {
+
+template <typename T, int D, bool Q4>
+int launch_append(const AppendParams& p, cudaStream_t st) {
+  kv_append_kernel<T, D, Q4><<<unsigned(p.tb.n_tokens), 256, 0, st>>>(p);
+  return launched(1);
+}
+
+template <bool Q4>
+int append_entry(const hils_dims* d, const hils_tokens* tk, const hils_rotary* ro, const hils_rows* q,
+                 const hils_rows* q_out, const hils_rows* k, const hils_rows* v, void* k_pages, void* v_pages,
+                 const int32_t* page_table, int64_t n_pages, hils_stream_t stream) {
+  AppendParams p;
+  int rc = check_tokens(d, tk, &p.tb);
+  if (rc) return rc;
+  if (n_pages < 1) return HILS_ERR_INVALID_ARGUMENT;
+  p.rotary = nullptr;
+  p.n_pos = 0;
+  p.rot = p.interleaved = 0;
+  if (ro != nullptr) {
+    if (ro->rot_dim < 16 || ro->rot_dim % 16 != 0 || ro->rot_dim > d->head_dim || ro->n_pos < 1 || !ptr_ok(ro->table) ||
+        (ro->interleaved != 0 && ro->interleaved != 1))
+      return HILS_ERR_INVALID_ARGUMENT;
+    p.rotary = ro->table;
+    p.n_pos = ro->n_pos;
+    p.rot = ro->rot_dim;
+    p.interleaved = ro->interleaved;
+  }
+  if ((q == nullptr) != (q_out == nullptr)) return HILS_ERR_INVALID_ARGUMENT;
+  if (p.tb.n_tokens == 0) return HILS_OK;
+  const int64_t T = p.tb.n_tokens;
+  if (q != nullptr && (!rows_ok(q, d, T, d->heads_q, false) || !rows_ok(q_out, d, T, d->heads_q, true)))
+    return HILS_ERR_INVALID_ARGUMENT;
+  if (!rows_ok(k, d, T, d->heads_kv, false) || !rows_ok(v, d, T, d->heads_kv, false) || !ptr_ok(k_pages) ||
+      !ptr_ok(v_pages) || !ptr_ok(page_table))
+    return HILS_ERR_INVALID_ARGUMENT;
+  p.q = rows_view(q);
+  p.q_out = rows_view(q_out);
+  p.k = rows_view(k);
+  p.v = rows_view(v);
+  p.k_pages = k_pages;
+  p.v_pages = v_pages;
+  p.table = page_table;
+  p.n_pages = n_pages;
+  p.nc = d->seqlen / kChunk;
+  p.Hq = d->heads_q;
+  p.Hkv = d->heads_kv;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (d->dtype == HILS_BF16)
+    return d->head_dim == 64 ? launch_append<__nv_bfloat16, 64, Q4>(p, st) : launch_append<__nv_bfloat16, 128, Q4>(p, st);
+  return d->head_dim == 64 ? launch_append<float, 64, Q4>(p, st) : launch_append<float, 128, Q4>(p, st);
+}
+
+template <typename T, int D, typename Rows>
+int launch_summary_append(SummaryParams p, cudaStream_t st) {
+  p.tau = 1.f / sqrtf(float(D));
+  const int64_t units = (p.tb.n_tokens + p.unit - 1) / p.unit * p.Hkv;
+  summary_append_kernel<T, D, Rows><<<unsigned((units + 3) / 4), 128, 0, st>>>(p);
+  return launched(1);
+}
+
+template <bool Q4>
+int summary_append_entry(const hils_dims* d, const hils_tokens* tk, const void* k_pages, const int32_t* page_table,
+                         int64_t n_pages, const void* lq, float* kprime, float* bprime, void* kprime_mma,
+                         hils_stream_t stream) {
+  SummaryParams p;
+  int rc = check_tokens(d, tk, &p.tb);
+  if (rc) return rc;
+  if (n_pages < 1) return HILS_ERR_INVALID_ARGUMENT;
+  if (kprime_mma != nullptr && d->dtype != HILS_BF16) return HILS_ERR_INVALID_ARGUMENT;
+  if (p.tb.n_tokens == 0) return HILS_OK;
+  if (!ptr_ok(k_pages) || !ptr_ok(page_table) || !ptr_ok(lq) || !ptr_ok(kprime) || !ptr_ok(bprime) ||
+      !aligned16(kprime_mma))
+    return HILS_ERR_INVALID_ARGUMENT;
+  p.k_pages = static_cast<const uint8_t*>(k_pages);
+  p.table = page_table;
+  p.n_pages = n_pages;
+  p.nc = d->seqlen / kChunk;
+  p.lq = lq;
+  p.kp = kprime;
+  p.bp = bprime;
+  p.kmma = static_cast<__nv_bfloat16*>(kprime_mma);
+  p.Hkv = d->heads_kv;
+  // as many tokens as a sequence has on average, up to a chunk: a warp then
+  // meets about one completed chunk at most
+  const int64_t mean = p.tb.n_tokens / d->batch;
+  p.unit = mean < 1 ? 1 : mean > kChunk ? kChunk : mean;
+  if ((p.tb.n_tokens / p.unit + 1) * p.Hkv >= (int64_t(1) << 33)) return HILS_ERR_UNSUPPORTED;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  using bf16 = __nv_bfloat16;
+  if constexpr (Q4) {
+    if (d->dtype == HILS_BF16)
+      return d->head_dim == 64 ? launch_summary_append<bf16, 64, QuantRows<bf16, 64>>(p, st)
+                               : launch_summary_append<bf16, 128, QuantRows<bf16, 128>>(p, st);
+    return d->head_dim == 64 ? launch_summary_append<float, 64, QuantRows<float, 64>>(p, st)
+                             : launch_summary_append<float, 128, QuantRows<float, 128>>(p, st);
+  } else {
+    if (d->dtype == HILS_BF16)
+      return d->head_dim == 64 ? launch_summary_append<bf16, 64, DenseRows<bf16, 64>>(p, st)
+                               : launch_summary_append<bf16, 128, DenseRows<bf16, 128>>(p, st);
+    return d->head_dim == 64 ? launch_summary_append<float, 64, DenseRows<float, 64>>(p, st)
+                             : launch_summary_append<float, 128, DenseRows<float, 128>>(p, st);
+  }
+}
+
+template <typename T, int D>
+int launch_decode_quant(const hils_dims* d, const void* q, const void* q_score, const void* kpg, const void* vpg,
+                        const int32_t* table, int64_t n_pages, const float* kp, const float* bp, const void* kmma,
+                        const int32_t* seqlens, void* o, int32_t* ids_out, float* scores_out, void* ws_ptr,
+                        cudaStream_t st) {
+  constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
+  const int64_t nc = d->seqlen / kChunk, rows = int64_t(d->batch) * d->heads_q;
+  const int G = d->heads_q / d->heads_kv, K = d->topk, wm1 = window_wm1(d), PS = K + wm1 + 1;
+  const float tau = 1.f / sqrtf(float(D));
+  DecodeWs ws;
+  decode_ws_layout(rows, nc, K, wm1 + 1, D, static_cast<char*>(ws_ptr), &ws);
+  const size_t smem1 = decode_scores_smem<D, BF>(G);
+  constexpr auto k1 = decode_scores_kernel<T, D, BF>;
+  if (smem1 > 48 * 1024 && set_smem_max<k1>() != cudaSuccess) return HILS_ERR_CUDA;
+  dim3 g1(unsigned((nc + kDecChunksPerCta - 1) / kDecChunksPerCta), unsigned(d->batch * d->heads_kv));
+  k1<<<g1, kDecChunksPerCta, smem1, st>>>(static_cast<const T*>(q_score ? q_score : q), kp, bp,
+                                          static_cast<const __nv_bfloat16*>(kmma), seqlens, d->seqlen, nc, d->heads_q,
+                                          G, d->heads_kv, tau, ws.scores, wm1);
+  cudaError_t e = launch_pdl(decode_topk_kernel, dim3(unsigned(rows)), 256, 0, st, ws.scores, seqlens, d->seqlen, nc,
+                             d->heads_q, K, ws.sel_ids, ws.sel_scores, wm1);
+  if (e != cudaSuccess) return HILS_ERR_CUDA;
+  const int64_t items = rows * PS;
+  e = launch_pdl(decode_partial_quant_kernel<T, D>, dim3(unsigned((items + 3) / 4)), 128, 0, st,
+                 static_cast<const T*>(q), static_cast<const uint8_t*>(kpg), static_cast<const uint8_t*>(vpg), table,
+                 n_pages, seqlens, d->seqlen, d->heads_q, G, d->heads_kv, K, tau,
+                 static_cast<const int32_t*>(ws.sel_ids), static_cast<const float*>(ws.sel_scores), ws.part_u,
+                 ws.part_o, items, wm1);
+  if (e != cudaSuccess) return HILS_ERR_CUDA;
+  e = launch_pdl(decode_combine_kernel<T, D>, dim3(unsigned(rows)), D, 0, st,
+                 static_cast<const float*>(ws.part_u), static_cast<const float*>(ws.part_o), seqlens, d->seqlen,
+                 d->heads_q, K, static_cast<const int32_t*>(ws.sel_ids), static_cast<const float*>(ws.sel_scores),
+                 static_cast<T*>(o), ids_out, scores_out, rows, wm1);
+  if (e != cudaSuccess) return HILS_ERR_CUDA;
+  return launched(4);
+}
+
+}  // namespace
+
+extern "C" {
+
+int hils_kv_append_paged(const hils_dims* d, const hils_tokens* tokens, const hils_rotary* rotary, const hils_rows* q,
+                         const hils_rows* q_out, const hils_rows* k, const hils_rows* v, void* k_pages, void* v_pages,
+                         const int32_t* page_table, int64_t n_pages, hils_stream_t stream) {
+  return append_entry<false>(d, tokens, rotary, q, q_out, k, v, k_pages, v_pages, page_table, n_pages, stream);
+}
+
+int hils_kv_append_quant(const hils_dims* d, const hils_tokens* tokens, const hils_rotary* rotary, const hils_rows* q,
+                         const hils_rows* q_out, const hils_rows* k, const hils_rows* v, void* k_pages, void* v_pages,
+                         const int32_t* page_table, int64_t n_pages, hils_stream_t stream) {
+  return append_entry<true>(d, tokens, rotary, q, q_out, k, v, k_pages, v_pages, page_table, n_pages, stream);
+}
+
+size_t hils_quant_page_bytes(const hils_dims* d) {
+  if (check_dims(d) != HILS_OK) return 0;
+  return size_t(d->heads_kv) * size_t(d->head_dim == 64 ? QuantPage<64>::BLOCK : QuantPage<128>::BLOCK);
+}
+
+int hils_kv_read_quant(const hils_dims* d, const hils_tokens* tokens, const void* k_pages, const void* v_pages,
+                       const int32_t* page_table, int64_t n_pages, const hils_rows* k, const hils_rows* v,
+                       hils_stream_t stream) {
+  ReadParams p;
+  int rc = check_tokens(d, tokens, &p.tb);
+  if (rc) return rc;
+  if (n_pages < 1 || (k == nullptr && v == nullptr)) return HILS_ERR_INVALID_ARGUMENT;
+  const int64_t T = p.tb.n_tokens;
+  if (T == 0) return HILS_OK;
+  if ((k != nullptr && (!rows_ok(k, d, T, d->heads_kv, true) || !ptr_ok(k_pages))) ||
+      (v != nullptr && (!rows_ok(v, d, T, d->heads_kv, true) || !ptr_ok(v_pages))) || !ptr_ok(page_table))
+    return HILS_ERR_INVALID_ARGUMENT;
+  p.k = rows_view(k);
+  p.v = rows_view(v);
+  p.k_pages = static_cast<const uint8_t*>(k_pages);
+  p.v_pages = static_cast<const uint8_t*>(v_pages);
+  p.table = page_table;
+  p.n_pages = n_pages;
+  p.nc = d->seqlen / kChunk;
+  p.Hkv = d->heads_kv;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const unsigned grid = unsigned(T);
+  if (d->dtype == HILS_BF16) {
+    if (d->head_dim == 64) kv_read_quant_kernel<__nv_bfloat16, 64><<<grid, 256, 0, st>>>(p);
+    else kv_read_quant_kernel<__nv_bfloat16, 128><<<grid, 256, 0, st>>>(p);
+  } else {
+    if (d->head_dim == 64) kv_read_quant_kernel<float, 64><<<grid, 256, 0, st>>>(p);
+    else kv_read_quant_kernel<float, 128><<<grid, 256, 0, st>>>(p);
+  }
+  return launched(1);
+}
+
+int hils_landmark_summary_append(const hils_dims* d, const hils_tokens* tokens, const void* k_pages,
+                                 const int32_t* page_table, int64_t n_pages, const void* lq, float* kprime,
+                                 float* bprime, void* kprime_mma, hils_stream_t stream) {
+  return summary_append_entry<false>(d, tokens, k_pages, page_table, n_pages, lq, kprime, bprime, kprime_mma, stream);
+}
+
+int hils_landmark_summary_quant(const hils_dims* d, const hils_tokens* tokens, const void* k_pages,
+                                const int32_t* page_table, int64_t n_pages, const void* lq, float* kprime,
+                                float* bprime, void* kprime_mma, hils_stream_t stream) {
+  return summary_append_entry<true>(d, tokens, k_pages, page_table, n_pages, lq, kprime, bprime, kprime_mma, stream);
+}
+
+size_t hils_decode_quant_workspace_bytes(const hils_dims* d) { return hils_decode_workspace_bytes(d); }
+
+int hils_attn_decode_quant(const hils_dims* d, const void* q, const void* q_score, const void* k_pages,
+                           const void* v_pages, const int32_t* page_table, int64_t n_pages, const float* kprime,
+                           const float* bprime, const void* kprime_mma, const int32_t* seqlens, void* o,
+                           int32_t* ids_out, float* scores_out, void* workspace, size_t workspace_bytes,
+                           hils_stream_t stream) {
+  int rc = check_dims(d);
+  if (rc) return rc;
+  if (d->heads_q / d->heads_kv > 32) return HILS_ERR_UNSUPPORTED;
+  if (int64_t(d->batch) * d->heads_kv > 65535) return HILS_ERR_UNSUPPORTED;   // the scoring grid's second dimension
+  if (!ptr_ok(q) || !aligned16(q_score) || !ptr_ok(k_pages) || !ptr_ok(v_pages) || !ptr_ok(page_table) ||
+      n_pages < 1 || !ptr_ok(seqlens) || !ptr_ok(o) || !aligned16(ids_out) || !aligned16(scores_out))
+    return HILS_ERR_INVALID_ARGUMENT;
+  if (d->dtype == HILS_BF16 ? !ptr_ok(kprime_mma) : (!ptr_ok(kprime) || !ptr_ok(bprime))) return HILS_ERR_INVALID_ARGUMENT;
+  if (workspace_bytes < hils_decode_quant_workspace_bytes(d)) return HILS_ERR_WORKSPACE_TOO_SMALL;
+  if (!ptr_ok(workspace)) return HILS_ERR_INVALID_ARGUMENT;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (d->dtype == HILS_BF16) {
+    if (d->head_dim == 64)
+      return launch_decode_quant<__nv_bfloat16, 64>(d, q, q_score, k_pages, v_pages, page_table, n_pages, nullptr, nullptr, kprime_mma, seqlens, o, ids_out, scores_out, workspace, st);
+    return launch_decode_quant<__nv_bfloat16, 128>(d, q, q_score, k_pages, v_pages, page_table, n_pages, nullptr, nullptr, kprime_mma, seqlens, o, ids_out, scores_out, workspace, st);
+  }
+  if (d->head_dim == 64)
+    return launch_decode_quant<float, 64>(d, q, q_score, k_pages, v_pages, page_table, n_pages, kprime, bprime, nullptr, seqlens, o, ids_out, scores_out, workspace, st);
+  return launch_decode_quant<float, 128>(d, q, q_score, k_pages, v_pages, page_table, n_pages, kprime, bprime, nullptr, seqlens, o, ids_out, scores_out, workspace, st);
 }
 
 size_t hils_attn_backward_workspace_bytes(const hils_dims* d) {

@@ -24,6 +24,9 @@ EXPORTS = ("hils_landmark_summary", "hils_kprime_mma_bytes", "hils_select", "hil
            "hils_decode_workspace_bytes", "hils_attn_decode", "hils_attn_decode_fixed_scratch",
            "hils_landmark_summary_paged", "hils_attn_decode_paged", "hils_query_calibrate", "hils_attn_decode_qcal",
            "hils_attn_backward_workspace_bytes", "hils_attn_backward",
+           "hils_kv_append_paged", "hils_kv_append_quant", "hils_quant_page_bytes", "hils_kv_read_quant",
+           "hils_landmark_summary_append", "hils_landmark_summary_quant",
+           "hils_decode_quant_workspace_bytes", "hils_attn_decode_quant",
            "hils_get_status", "hils_selftest_bounded_wait", "hils_strerror", "hils_kernel_launches")
 DECODE_FIXED_SCRATCH_BYTES = 16 << 20
 
@@ -38,6 +41,19 @@ class hils_dims(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int32), ("heads_q", ctypes.c_int32), ("heads_kv", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32), ("chunk", ctypes.c_int32), ("topk", ctypes.c_int32),
                 ("seqlen", ctypes.c_int64), ("dtype", ctypes.c_int32), ("window", ctypes.c_int32)]
+
+
+class hils_tokens(ctypes.Structure):
+    _fields_ = [("n_tokens", ctypes.c_int64), ("cu_tokens", ctypes.c_void_p), ("seqlens", ctypes.c_void_p)]
+
+
+class hils_rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class hils_rotary(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("n_pos", ctypes.c_int64), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32)]
 
 
 _lib = None
@@ -70,6 +86,16 @@ def lib():
         L.hils_attn_backward_workspace_bytes.argtypes = [D]
         L.hils_attn_backward_workspace_bytes.restype = SZ
         L.hils_attn_backward.argtypes = [D, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, SZ, P]
+        L.hils_kv_append_paged.argtypes = [D, P, P, P, P, P, P, P, P, P, I64, P]
+        L.hils_kv_append_quant.argtypes = [D, P, P, P, P, P, P, P, P, P, I64, P]
+        L.hils_quant_page_bytes.argtypes = [D]
+        L.hils_quant_page_bytes.restype = SZ
+        L.hils_kv_read_quant.argtypes = [D, P, P, P, P, I64, P, P, P]
+        L.hils_landmark_summary_append.argtypes = [D, P, P, P, I64, P, P, P, P, P]
+        L.hils_landmark_summary_quant.argtypes = [D, P, P, P, I64, P, P, P, P, P]
+        L.hils_decode_quant_workspace_bytes.argtypes = [D]
+        L.hils_decode_quant_workspace_bytes.restype = SZ
+        L.hils_attn_decode_quant.argtypes = [D, P, P, P, P, P, I64, P, P, P, P, P, P, P, P, SZ, P]
         L.hils_get_status.argtypes = [ctypes.POINTER(ctypes.c_int32), P]
         L.hils_selftest_bounded_wait.argtypes = [ctypes.c_int32, P]
         L.hils_strerror.argtypes = [ctypes.c_int]
@@ -83,6 +109,13 @@ def lib():
 
 def strerror(status: int) -> str:
     return lib().hils_strerror(int(status)).decode()
+
+
+def _on_current_device(t):
+    if not t.is_cuda:
+        raise ValueError(f"expected a CUDA tensor, got one on {t.device}")
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"tensor on {t.device} but the current device is cuda:{torch.cuda.current_device()}")
 
 
 def _ptr(t):
@@ -245,6 +278,80 @@ def hils_attn_backward(dims, q, q_score, k, v, lq, kprime, ids, scores, lse_own,
                                     int(nbytes), _stream(stream)))
 
 
+def _rows(t):
+    """hils_rows of a tensor [T, heads, d] whose last dimension is dense (None is passed on)."""
+    if t is None:
+        return None
+    _on_current_device(t)
+    if t.dim() != 3 or t.stride(2) != 1:
+        raise ValueError(f"expected rows [T, heads, d] with a dense last dimension, got shape {tuple(t.shape)} with "
+                         f"strides {t.stride()}")
+    return ctypes.byref(hils_rows(t.data_ptr(), t.stride(0), t.stride(1)))
+
+
+def _tokens(seqlens, n_tokens, cu_tokens):
+    cu = None if cu_tokens is None else _ptr(cu_tokens)
+    return ctypes.byref(hils_tokens(int(n_tokens), cu, _ptr(seqlens)))
+
+
+def hils_kv_append_paged(dims, seqlens, n_tokens, cu_tokens, rotary, q, q_out, k, v, k_pages, v_pages, page_table,
+                         n_pages, stream=None):
+    """rotary: a Rotary or None; q, q_out, k, v: rows [T, heads, d] with any token and head stride."""
+    _check("hils_kv_append_paged",
+           lib().hils_kv_append_paged(ctypes.byref(dims), _tokens(seqlens, n_tokens, cu_tokens), _rotary(rotary),
+                                      _rows(q), _rows(q_out), _rows(k), _rows(v), _ptr(k_pages), _ptr(v_pages),
+                                      _ptr(page_table), int(n_pages), _stream(stream)))
+
+
+def hils_kv_append_quant(dims, seqlens, n_tokens, cu_tokens, rotary, q, q_out, k, v, k_pages, v_pages, page_table,
+                         n_pages, stream=None):
+    _check("hils_kv_append_quant",
+           lib().hils_kv_append_quant(ctypes.byref(dims), _tokens(seqlens, n_tokens, cu_tokens), _rotary(rotary),
+                                      _rows(q), _rows(q_out), _rows(k), _rows(v), _ptr(k_pages), _ptr(v_pages),
+                                      _ptr(page_table), int(n_pages), _stream(stream)))
+
+
+def hils_quant_page_bytes(dims) -> int:
+    return int(lib().hils_quant_page_bytes(ctypes.byref(dims)))
+
+
+def hils_kv_read_quant(dims, seqlens, n_tokens, cu_tokens, k_pages, v_pages, page_table, n_pages, k, v, stream=None):
+    _check("hils_kv_read_quant",
+           lib().hils_kv_read_quant(ctypes.byref(dims), _tokens(seqlens, n_tokens, cu_tokens), _ptr(k_pages),
+                                    _ptr(v_pages), _ptr(page_table), int(n_pages), _rows(k), _rows(v),
+                                    _stream(stream)))
+
+
+def hils_landmark_summary_append(dims, seqlens, n_tokens, cu_tokens, k_pages, page_table, n_pages, lq, kprime, bprime,
+                                 kprime_mma=None, stream=None):
+    _check("hils_landmark_summary_append",
+           lib().hils_landmark_summary_append(ctypes.byref(dims), _tokens(seqlens, n_tokens, cu_tokens), _ptr(k_pages),
+                                              _ptr(page_table), int(n_pages), _ptr(lq), _ptr(kprime), _ptr(bprime),
+                                              _ptr(kprime_mma), _stream(stream)))
+
+
+def hils_landmark_summary_quant(dims, seqlens, n_tokens, cu_tokens, k_pages, page_table, n_pages, lq, kprime, bprime,
+                                kprime_mma=None, stream=None):
+    _check("hils_landmark_summary_quant",
+           lib().hils_landmark_summary_quant(ctypes.byref(dims), _tokens(seqlens, n_tokens, cu_tokens), _ptr(k_pages),
+                                             _ptr(page_table), int(n_pages), _ptr(lq), _ptr(kprime), _ptr(bprime),
+                                             _ptr(kprime_mma), _stream(stream)))
+
+
+def hils_decode_quant_workspace_bytes(dims) -> int:
+    return int(lib().hils_decode_quant_workspace_bytes(ctypes.byref(dims)))
+
+
+def hils_attn_decode_quant(dims, q, q_score, k_pages, v_pages, page_table, n_pages, kprime, bprime, kprime_mma,
+                           seqlens, o, ids_out, scores_out, workspace, workspace_bytes=None, stream=None):
+    nbytes = workspace.numel() * workspace.element_size() if workspace_bytes is None else workspace_bytes
+    _check("hils_attn_decode_quant",
+           lib().hils_attn_decode_quant(ctypes.byref(dims), _ptr(q), _ptr(q_score), _ptr(k_pages), _ptr(v_pages),
+                                        _ptr(page_table), int(n_pages), _ptr(kprime), _ptr(bprime), _ptr(kprime_mma),
+                                        _ptr(seqlens), _ptr(o), _ptr(ids_out), _ptr(scores_out), _ptr(workspace),
+                                        int(nbytes), _stream(stream)))
+
+
 def hils_get_status(stream=None) -> int:
     v = ctypes.c_int32(0)
     _check("hils_get_status", lib().hils_get_status(ctypes.byref(v), _stream(stream)))
@@ -274,6 +381,14 @@ class Summary:
         if dims.dtype == BF16:
             n = hils_kprime_mma_bytes(dims)
             self.kprime_mma = torch.empty((n // 2,), dtype=torch.bfloat16, device=device)
+
+    @classmethod
+    def of(cls, kprime, bprime, kprime_mma=None):
+        """The summaries in tensors that the caller holds: fp32 [B,Hkv,nc,d] and [B,Hkv,nc], and for bf16 the scoring
+        operand [B,Hkv,nc,d+16] (or flat)."""
+        self = cls.__new__(cls)
+        self.kprime, self.bprime, self.kprime_mma = kprime, bprime, kprime_mma
+        return self
 
 
 def landmark_summary(k, lq, topk=1, chunk_begin=0, chunk_end=None, out: Summary | None = None, stream=None):
@@ -388,3 +503,193 @@ def decode_step(q, k_cache, v_cache, summ: Summary, seqlens, topk, workspace=Non
     hils_attn_decode(dims, q, k_cache, v_cache, summ.kprime, summ.bprime, summ.kprime_mma, seqlens, o, ids, scores,
                      workspace, stream=stream)
     return o, ids, scores
+
+
+# ---------------------------------------------------------------------------
+# Serving from a chunk-paged cache: pages in bf16 / fp32 [n_pages,Hkv,64,d], or in 4 bits as uint8
+# [n_pages,Hkv,64*(d/2+d/8)]; page_table int32 [B,nc].  A ragged batch of new tokens is packed [T]; seqlens int32 [B]
+# are the lengths after the append, cu_tokens int32 [B+1] the sequences' places in it (None: T/B tokens each).
+#
+# stream: the kernels run there, and so are the outputs that a call makes; its inputs must be ready on it.
+
+class Rotary:
+    """A rotary position table fp32 [n_pos, rot_dim] (cosines, then sines of rot_dim/2 angles) and the pairing of
+    dims: the halves of the first rot_dim dims, or neighbours (interleaved)."""
+    __slots__ = ("table", "interleaved")
+
+    def __init__(self, table, interleaved=False):
+        _need(table, "rotary table", torch.float32, (None, None))
+        self.table, self.interleaved = table, bool(interleaved)
+
+
+def rotary_table(n_pos, rot_dim, base=10000.0, device="cuda"):
+    """Cosines and sines of pos * base^(-2i/rot_dim) for a Rotary, angles computed in fp64 (far positions lose their
+    phase in fp32)."""
+    freq = float(base) ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device) / rot_dim)
+    angle = torch.arange(n_pos, dtype=torch.float64, device=device)[:, None] * freq
+    return torch.cat([angle.cos(), angle.sin()], 1).float()
+
+
+def _rotary(r):
+    if r is None:
+        return None
+    n_pos, rot = r.table.shape
+    return ctypes.byref(hils_rotary(_ptr(r.table), n_pos, rot, int(r.interleaved)))
+
+
+def _need(t, name, dtype, shape):
+    """Refuse a tensor of another type or shape (None: any extent)."""
+    if t.dtype != dtype or t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError(f"{name}: expected {dtype} {tuple('any' if n is None else n for n in shape)}, got {t.dtype} "
+                         f"{tuple(t.shape)}")
+
+
+def _page_kind(k_pages, v_pages, dtype):
+    """(4-bit?, n_pages, Hkv, d) of a pair of pools (v_pages None: keys alone)."""
+    if v_pages is not None and (v_pages.shape != k_pages.shape or v_pages.dtype != k_pages.dtype):
+        raise ValueError(f"key pages {k_pages.dtype} {tuple(k_pages.shape)} and value pages {v_pages.dtype} "
+                         f"{tuple(v_pages.shape)} differ")
+    if k_pages.dtype == torch.uint8:
+        if k_pages.dim() != 3 or k_pages.shape[2] not in (40 * CHUNK, 80 * CHUNK):
+            raise ValueError(f"4-bit pages are [n_pages, Hkv, 64 * (d/2 + d/8)], got {tuple(k_pages.shape)}")
+        return True, k_pages.shape[0], k_pages.shape[1], k_pages.shape[2] // 40
+    if k_pages.dim() != 4 or k_pages.shape[2] != CHUNK or k_pages.dtype != dtype:
+        raise ValueError(f"expected {dtype} pages [n_pages, Hkv, 64, d] or 4-bit ones, got {k_pages.dtype} "
+                         f"{tuple(k_pages.shape)}")
+    return False, k_pages.shape[0], k_pages.shape[1], k_pages.shape[3]
+
+
+def _batch(page_table, seqlens, cu_tokens):
+    """(B, nc) of a ragged batch."""
+    _need(page_table, "page_table", torch.int32, (None, None))
+    B, nc = page_table.shape
+    _need(seqlens, "seqlens", torch.int32, (B,))
+    if cu_tokens is not None:
+        _need(cu_tokens, "cu_tokens", torch.int32, (B + 1,))
+    return B, nc
+
+
+class _on:
+    """Allocate on the stream that the kernels will run on, so that the caching allocator gives the memory to no other
+    stream's work before they end."""
+
+    def __init__(self, stream):
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream)
+        self.ctx = None if stream is None else torch.cuda.stream(stream)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def quant_pages(n_pages, heads_kv, head_dim, device="cuda"):
+    """A pool of 4-bit pages (of keys, or of values)."""
+    dims = make_dims(1, heads_kv, heads_kv, head_dim, CHUNK, 1, BF16)
+    n = hils_quant_page_bytes(dims)
+    if not n:
+        raise ValueError(f"head_dim {head_dim} is not supported")
+    return torch.zeros((n_pages, heads_kv, n // heads_kv), dtype=torch.uint8, device=device)
+
+
+def kv_append(k_pages, v_pages, page_table, k, v, seqlens, cu_tokens=None, rotary=None, q=None, q_out=None,
+              stream=None):
+    """Append the packed new keys and values k, v [T,Hkv,d] to a chunk-paged cache (bf16 / fp32 or 4-bit pages),
+    rotating keys, and queries q [T,Hq,d], by their positions.  k, v, q may be views with any token and head stride.
+    Returns the rotated queries (q_out, or a new [T,Hq,d]; None without q)."""
+    quant, n_pages, Hkv, d = _page_kind(k_pages, v_pages, k.dtype)
+    B, nc = _batch(page_table, seqlens, cu_tokens)
+    T = k.shape[0]
+    _need(k, "k", k.dtype, (T, Hkv, d))
+    _need(v, "v", k.dtype, (T, Hkv, d))
+    Hq = Hkv
+    if q is not None:
+        Hq = q.shape[1]
+        _need(q, "q", k.dtype, (T, Hq, d))
+        if q_out is None:
+            with _on(stream):
+                q_out = torch.empty((T, Hq, d), dtype=k.dtype, device=k.device)
+        else:
+            _need(q_out, "q_out", k.dtype, (T, Hq, d))
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    dims = make_dims(B, Hq, Hkv, d, nc * CHUNK, 1, k.dtype)
+    call = hils_kv_append_quant if quant else hils_kv_append_paged
+    call(dims, seqlens, T, cu_tokens, rotary, q, q_out, k, v, k_pages, v_pages, page_table, n_pages, stream)
+    return q_out
+
+
+def kv_read(k_pages, v_pages, page_table, seqlens, n_tokens, dtype, cu_tokens=None, k_out=None, v_out=None,
+            stream=None):
+    """The last n_b cached rows of every sequence of a 4-bit cache as (k, v) [T,Hkv,d] of `dtype`; k_out, v_out may
+    have any token and head stride, e.g. cache[0].transpose(0, 1) of a contiguous cache [1,Hkv,N,d]."""
+    quant, n_pages, Hkv, d = _page_kind(k_pages, v_pages, dtype)
+    if not quant:
+        raise ValueError("kv_read reads 4-bit pages")
+    B, nc = _batch(page_table, seqlens, cu_tokens)
+    out = []
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        if t is None:
+            with _on(stream):
+                t = torch.empty((n_tokens, Hkv, d), dtype=dtype, device=k_pages.device)
+        else:
+            _need(t, name, dtype, (n_tokens, Hkv, d))
+        out.append(t)
+    dims = make_dims(B, Hkv, Hkv, d, nc * CHUNK, 1, dtype)
+    hils_kv_read_quant(dims, seqlens, n_tokens, cu_tokens, k_pages, v_pages, page_table, n_pages, *out, stream)
+    return tuple(out)
+
+
+def _need_summary(summ, B, Hkv, nc, d, dtype):
+    _need(summ.kprime, "kprime", torch.float32, (B, Hkv, nc, d))
+    _need(summ.bprime, "bprime", torch.float32, (B, Hkv, nc))
+    if dtype == torch.bfloat16:
+        m = summ.kprime_mma
+        if m is None or m.dtype != torch.bfloat16 or m.numel() != B * Hkv * nc * (d + 16):
+            raise ValueError(f"kprime_mma: expected the bf16 scoring operand of {B * Hkv * nc * (d + 16)} elements")
+
+
+def landmark_summary_append(k_pages, page_table, lq, seqlens, n_tokens, summ: Summary, cu_tokens=None, stream=None):
+    """Write the summaries of the chunks that an append of n_tokens packed tokens completed into summ; lq
+    [B,Hkv,nc,d].  k_pages in lq's type or in 4 bits."""
+    quant, n_pages, Hkv, d = _page_kind(k_pages, None, lq.dtype)
+    B, nc = _batch(page_table, seqlens, cu_tokens)
+    _need(lq, "lq", lq.dtype, (B, Hkv, nc, d))
+    _need_summary(summ, B, Hkv, nc, d, lq.dtype)
+    dims = make_dims(B, Hkv, Hkv, d, nc * CHUNK, 1, lq.dtype)
+    call = hils_landmark_summary_quant if quant else hils_landmark_summary_append
+    call(dims, seqlens, n_tokens, cu_tokens, k_pages, page_table, n_pages, lq, summ.kprime, summ.bprime,
+         summ.kprime_mma, stream)
+    return summ
+
+
+def decode_step_quant(q, k_pages, v_pages, page_table, summ: Summary, seqlens, topk, q_score=None, workspace=None,
+                      stream=None, window=0, out=None):
+    """One decode step for q [B,Hq,d] against a 4-bit chunk-paged cache; q_score: a separate scoring query (Q-Cal).
+    Returns (o, ids, scores)."""
+    B, Hq, d = q.shape
+    quant, n_pages, Hkv, d_pages = _page_kind(k_pages, v_pages, q.dtype)
+    if not quant:
+        raise ValueError("decode_step_quant reads 4-bit pages")
+    _, nc = _batch(page_table, seqlens, None)
+    _need(q, "q", q.dtype, (page_table.shape[0], None, d_pages))
+    if q_score is not None:
+        _need(q_score, "q_score", q.dtype, (B, Hq, d))
+    _need_summary(summ, B, Hkv, nc, d, q.dtype)
+    dims = make_dims(B, Hq, Hkv, d, nc * CHUNK, topk, q.dtype, window=window)
+    with _on(stream):
+        if workspace is None:
+            workspace = torch.empty((hils_decode_quant_workspace_bytes(dims),), dtype=torch.uint8, device=q.device)
+        if out is None:
+            out = torch.empty_like(q)
+        else:
+            _need(out, "out", q.dtype, (B, Hq, d))
+        ids = torch.empty((B, Hq, topk), dtype=torch.int32, device=q.device)
+        scores = torch.empty((B, Hq, topk), dtype=torch.float32, device=q.device)
+    hils_attn_decode_quant(dims, q, q_score, k_pages, v_pages, page_table, n_pages, summ.kprime, summ.bprime,
+                           summ.kprime_mma, seqlens, out, ids, scores, workspace, stream=stream)
+    return out, ids, scores

@@ -324,6 +324,146 @@ int hils_attn_decode_qcal(const hils_dims* dims, const void* q, const void* q_sc
                           const int32_t* seqlens, void* o, int32_t* ids_out, float* scores_out,
                           void* workspace, size_t workspace_bytes, hils_stream_t stream);
 
+/*
+ * Serving from a chunk-paged cache: appending new tokens, the summaries of
+ * the chunks they complete, and a cache held in 4 bits.  The three kinds of
+ * call share one description of the ragged batch:
+ */
+typedef struct hils_tokens {
+  int64_t n_tokens;          /* T: packed new tokens, 0 .. 2^31 - 1 (0: the call
+                                does nothing) */
+  const int32_t* cu_tokens;  /* device int32 [B+1], ascending from 0: sequence b
+                                has the packed tokens cu_tokens[b] ..
+                                cu_tokens[b+1]-1 (none is allowed).  Tokens
+                                from cu_tokens[B] on are padding: skipped, the
+                                rows they would write stay as they were.  NULL:
+                                T / B tokens of every sequence. */
+  const int32_t* seqlens;    /* device int32 [B]: lengths AFTER the append (what
+                                the decode step takes), 0 .. dims.seqlen.  The
+                                new tokens of b are its positions
+                                seqlens[b] - n_b .. seqlens[b] - 1. */
+} hils_tokens;
+
+/* Rows [T, heads, d] of `dtype`, d innermost and dense, with any token and
+ * head stride in elements (a view of a fused projection, or head-major).
+ * data 16-byte aligned, strides non-negative multiples of 16 bytes; the rows
+ * of an output must not overlap (HILS_ERR_INVALID_ARGUMENT). */
+typedef struct hils_rows {
+  void* data;
+  int64_t token_stride;
+  int64_t head_stride;
+} hils_rows;
+
+/* Rotary position table: fp32 [n_pos, rot_dim], for each position rot_dim/2
+ * cosines and then rot_dim/2 sines.  The first rot_dim dims of every query
+ * and key head are rotated, the rest carry no position ([AIT-Meth]: HoPE keeps
+ * part of the rotation).  rot_dim: a multiple of 16, 16 .. d. */
+typedef struct hils_rotary {
+  const float* table;
+  int64_t n_pos;
+  int32_t rot_dim;
+  int32_t interleaved;  /* 0: dims i and i + rot_dim/2 form a pair; 1: dims 2i and 2i+1 */
+} hils_rotary;
+
+/*
+ * Append new keys and values to a chunk-paged cache (pages as in
+ * hils_attn_decode_paged), rotating keys and queries by their positions on
+ * the way -- the write side of [AIT-Tech]'s chunk-unit KV paging.  With x, y a
+ * pair and its position's cosine c and sine s:
+ *     x' = x c - y s,   y' = y c + x s       (fp32 arithmetic)
+ *   tokens        the new tokens
+ *   rotary        NULL: no rotation
+ *   q, q_out      [T, Hq, d] (both NULL: no queries); q_out may be q itself
+ *                 (same address and strides) but must not overlap it otherwise
+ *   k, v          [T, Hkv, d]
+ *   k_pages, v_pages  [n_pages, Hkv, C, d] dtype: the new positions' rows are
+ *                 written, nothing else
+ *   page_table    device int32 [B, seqlen/C]; the chunks of the new positions
+ *                 must have pages, no two of them the same page
+ * A token whose sequence description does not fit (seqlens[b] above the
+ * capacity or below n_b, cu_tokens not ascending or beyond T, a position
+ * outside the rotary table) is skipped; of one whose page is outside the pool
+ * only the query is written.  Both are recorded as HILS_ERR_DEVICE_BOUNDS.
+ */
+int hils_kv_append_paged(const hils_dims* dims, const hils_tokens* tokens, const hils_rotary* rotary,
+                         const hils_rows* q, const hils_rows* q_out, const hils_rows* k, const hils_rows* v,
+                         void* k_pages, void* v_pages, const int32_t* page_table, int64_t n_pages,
+                         hils_stream_t stream);
+
+/*
+ * The same append into a cache held in 4 bits.  A row (token, kv head) is
+ * split into groups of 32 dims; a group keeps
+ *     s = fp16((max - min) / 15),  m = fp16(min),
+ *     code = clamp(round((x - m) / s), 0, 15)     (s = 0: code 0)
+ * of the rotated fp32 values and stands for m + s * code.  A group with a
+ * value that is not finite, or with s or m beyond fp16, stands for NaN.
+ *   k_pages, v_pages  n_pages * hils_quant_page_bytes(dims) bytes each:
+ *       [n_pages, Hkv] blocks of C rows of d/2 bytes of codes followed by C
+ *       rows of d/32 (s, m) pairs in fp16.  In a row of codes the little-endian
+ *       16-bit unit e * (d/32) + g (0 <= e < 8) holds the codes of dims
+ *       32g + 4e .. 32g + 4e + 3, the lowest dim in the lowest 4 bits.
+ * Other arguments and errors as in hils_kv_append_paged.
+ */
+int hils_kv_append_quant(const hils_dims* dims, const hils_tokens* tokens, const hils_rotary* rotary,
+                         const hils_rows* q, const hils_rows* q_out, const hils_rows* k, const hils_rows* v,
+                         void* k_pages, void* v_pages, const int32_t* page_table, int64_t n_pages,
+                         hils_stream_t stream);
+
+/* Bytes of one 4-bit page of keys (or of values): Hkv * C * (d/2 + d/8). */
+size_t hils_quant_page_bytes(const hils_dims* dims);
+
+/*
+ * Read rows of a 4-bit cache back: the positions that `tokens` describes (the
+ * last n_b of every sequence; cu_tokens as differences of seqlens reads whole
+ * sequences), as values m + s * code rounded to dtype -- a cached prefix for
+ * hils_attn_prefill, or a sequence moved to an unquantised cache.
+ *   k, v   [T, Hkv, d] out (either may be NULL)
+ * Tokens that cannot be placed, or whose page is outside the pool, are
+ * recorded as HILS_ERR_DEVICE_BOUNDS and their rows left as they were.
+ */
+int hils_kv_read_quant(const hils_dims* dims, const hils_tokens* tokens, const void* k_pages, const void* v_pages,
+                       const int32_t* page_table, int64_t n_pages, const hils_rows* k, const hils_rows* v,
+                       hils_stream_t stream);
+
+/*
+ * Landmark summaries of the chunks that an append completed: chunks
+ * floor((seqlens[b] - n_b) / C) .. floor(seqlens[b] / C) - 1 of every sequence
+ * b (none, for most sequences of a decode step) -- hils_landmark_summary_paged
+ * for a ragged batch whose lengths only the device knows.
+ *   tokens   the batch of the append
+ *   k_pages  chunk pages in dtype (hils_landmark_summary_append) or in 4 bits
+ *            (hils_landmark_summary_quant)
+ *   lq, kprime, bprime, kprime_mma  as in hils_landmark_summary; the other
+ *            chunks' summaries stay as they were
+ * A completed chunk whose page is outside the pool is recorded as
+ * HILS_ERR_DEVICE_BOUNDS and left unwritten.
+ */
+int hils_landmark_summary_append(const hils_dims* dims, const hils_tokens* tokens, const void* k_pages,
+                                 const int32_t* page_table, int64_t n_pages, const void* lq, float* kprime,
+                                 float* bprime, void* kprime_mma, hils_stream_t stream);
+int hils_landmark_summary_quant(const hils_dims* dims, const hils_tokens* tokens, const void* k_pages,
+                                const int32_t* page_table, int64_t n_pages, const void* lq, float* kprime,
+                                float* bprime, void* kprime_mma, hils_stream_t stream);
+
+/* Device workspace bytes hils_attn_decode_quant needs for these dims. */
+size_t hils_decode_quant_workspace_bytes(const hils_dims* dims);
+
+/*
+ * The decode step of hils_attn_decode over a 4-bit chunk-paged cache: scoring
+ * and selection from the summaries, attention over the values that the codes
+ * of the kept chunks and of the local window stand for.
+ *   q_score  scoring query as in hils_attn_decode_qcal, or NULL: q scores
+ *   k_pages, v_pages, page_table, n_pages  as hils_kv_append_quant fills them
+ *   workspace  at least hils_decode_quant_workspace_bytes(dims)
+ * Other arguments, results and errors as in hils_attn_decode_paged;
+ * B * Hkv <= 65535.
+ */
+int hils_attn_decode_quant(const hils_dims* dims, const void* q, const void* q_score, const void* k_pages,
+                           const void* v_pages, const int32_t* page_table, int64_t n_pages, const float* kprime,
+                           const float* bprime, const void* kprime_mma, const int32_t* seqlens, void* o,
+                           int32_t* ids_out, float* scores_out, void* workspace, size_t workspace_bytes,
+                           hils_stream_t stream);
+
 /* Device workspace bytes hils_attn_backward needs for these dims. */
 size_t hils_attn_backward_workspace_bytes(const hils_dims* dims);
 
