@@ -1,73 +1,709 @@
-// One decode step over a 4-bit chunk-paged cache: the scoring, top-K and
-// combine kernels of decode.cuh around a partial kernel that reads 4-bit pages.
+// One decode step over a 4-bit chunk-paged cache, in three kernels:
+//   Q1 scores : s^ of every candidate chunk (bf16: matrix instructions)
+//   Q2 top-K  : the K best chunks of every query row, ids ascending
+//   Q3 attend : the kept chunks' and the window's attention and their fusion
+// The readings (scores, ties, window, fusion) are those of decode.cuh.
+// Q2 and Q3 are launched with programmatic stream serialisation.
 #pragma once
+#include <cooperative_groups.h>
+
 #include "decode.cuh"
 #include "quant.cuh"
 
 namespace hils {
 
-// One warp per (row, slot): slots 0 .. K-1 are the row's kept chunks, K + w is
-// window chunk own - w.  Each key row is read by D / 8 lanes; an online
-// softmax per key group, merged by shuffles.
-template <typename T, int D>
-__global__ void __launch_bounds__(128)
-decode_partial_quant_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, const uint8_t* __restrict__ vpg,
-                            const int32_t* __restrict__ table, int64_t n_pages, const int32_t* __restrict__ seqlens,
-                            int64_t cap, int Hq, int G, int Hkv, int K, float tau, const int32_t* __restrict__ sel_ids,
-                            const float* __restrict__ sel_scores, float* __restrict__ part_u,
-                            float* __restrict__ part_o, int64_t n_items, int wm1) {
-  constexpr int E = 8, LPK = D / E, KPI = 32 / LPK;
-  pdl_wait();
-  pdl_trigger();
-  const int lane = threadIdx.x & 31, grp = lane / LPK, sub = lane % LPK, PS = K + wm1 + 1;
-  const int64_t item = (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  if (item >= n_items) return;
-  const int64_t row = item / PS;
-  const int slot = int(item % PS), b = int(row / Hq), h = int(row % Hq) / G;
-  const int64_t own = decode_own_chunk(seqlens, b, cap), nc = cap / kChunk;
-  int64_t c = -1;
-  if (own >= 0) {
-    if (slot >= K) {
-      c = own - (slot - K);
-    } else {
-      c = sel_ids[row * K + slot];
-      if (c >= 0 && c >= own - wm1) {
-        if (lane == 0) record_error(HILS_ERR_DEVICE_BOUNDS);
-        c = -1;
-      }
+// c += a b for 16x16 a (row) and 16x8 b (column), fp32 sums
+__device__ __forceinline__ void mma16816_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma16816_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// transpose of an 8x8 matrix of 16-bit values spread over the warp
+__device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+// the two bf16 values of a register in fp32
+__device__ __forceinline__ float lo_bf16(uint32_t x) { return __uint_as_float(x << 16); }
+__device__ __forceinline__ float hi_bf16(uint32_t x) { return __uint_as_float(x & 0xFFFF0000u); }
+
+// Four codes of two 16-bit units as bf16 pairs: 16 + code has the code in
+// bits 3 .. 6.  CENTRE: code - 8 instead, exactly (one subtraction more; the
+// products' sums then do not carry the offset, which fp32 results would feel).
+template <bool CENTRE>
+__device__ __forceinline__ void codes_bf16(uint32_t x, uint32_t (&a)[4]) {
+  a[0] = ((x << 3) & 0x00780078u) | 0x41804180u;
+  a[1] = ((x >> 1) & 0x00780078u) | 0x41804180u;
+  a[2] = ((x >> 5) & 0x00780078u) | 0x41804180u;
+  a[3] = ((x >> 9) & 0x00780078u) | 0x41804180u;
+  if constexpr (CENTRE) {
+    const __nv_bfloat162 c24 = __floats2bfloat162_rn(24.f, 24.f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a[i]), c24);
+      a[i] = *reinterpret_cast<const uint32_t*>(&v);
     }
   }
-  const int64_t off = c >= 0 ? quant_block_offset<D>(table, n_pages, b, h, c, Hkv, nc) : -1;
-  if (off < 0) {
-    if (lane == 0) part_u[row * PS + slot] = -INFINITY;
+}
+
+// ---------------------------------------------------------------- Q1
+// One warp scores 16 chunks against the query heads of a kv head, eight heads
+// per matrix instruction (rows: chunks, columns: heads).  The order of the
+// dims inside the sum is free, so each lane reads its operand rows in 16-byte
+// pieces (row lane/4 and lane/4 + 8, piece 4 c + lane % 4) and the queries in
+// the same order: no shared memory, all loads of the 16 rows in flight at
+// once.  HBM-bound: (d + 16) x 2 bytes per (kv head, candidate).
+template <int D>
+__global__ void __launch_bounds__(128)
+quant_scores_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ kmma,
+                    const int32_t* __restrict__ seqlens, int64_t cap, int64_t nc, int Hq, int G, int Hkv, float tau,
+                    float* __restrict__ ws_scores, int wm1) {
+  constexpr int NV = D / 32, RS = D + kExt;
+  pdl_trigger();
+  const int bh = blockIdx.y, b = bh / Hkv, h = bh % Hkv;
+  const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
+  const int64_t own = decode_own_chunk(seqlens, b, cap);
+  if (own < 0) {
+    if (threadIdx.x == 0 && blockIdx.x == 0) record_error(HILS_ERR_DEVICE_BOUNDS);
     return;
   }
-  const int n_keys = slot == K ? int(seqlens[b] - own * kChunk) : kChunk;
-  float qv[E];
-  const T* qr = q + row * D + sub * E;
+  const int64_t n_cand = own - wm1, c0 = (int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5)) * 16;
+  if (c0 >= n_cand) return;
+  const int64_t last = n_cand - 1;
+  const int64_t ca = c0 + gid < last ? c0 + gid : last, cb = c0 + gid + 8 < last ? c0 + gid + 8 : last;
+  const __nv_bfloat16 *ra = kmma + (int64_t(bh) * nc + ca) * RS, *rb = kmma + (int64_t(bh) * nc + cb) * RS;
+  uint4 xa[NV], xb[NV];
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    if constexpr (sizeof(T) == 2) qv[e] = __bfloat162float(qr[e]);
-    else qv[e] = qr[e];
+  for (int i = 0; i < NV; ++i) {
+    xa[i] = __ldg(reinterpret_cast<const uint4*>(ra + 32 * i + 8 * tig));
+    xb[i] = __ldg(reinterpret_cast<const uint4*>(rb + 32 * i + 8 * tig));
   }
-  SoftAcc<E> a;
-  a.init();
-  for (int r = grp; r < kChunk; r += KPI) {
-    float k[E], v[E], part = 0.f;
-    quant_load_row<D, E>(kpg + off, r, sub, k);
-    quant_load_row<D, E>(vpg + off, r, sub, v);
+  // b'/tau as the sum of two bf16 values
+  const uint32_t ea = __ldg(reinterpret_cast<const uint32_t*>(ra + D)), eb = __ldg(reinterpret_cast<const uint32_t*>(rb + D));
+  const float ba = lo_bf16(ea) + hi_bf16(ea), bb = lo_bf16(eb) + hi_bf16(eb);
+  for (int g0 = 0; g0 < G; g0 += 8) {
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    const bool have = g0 + gid < G;
+    const __nv_bfloat16* qr = q + (int64_t(b) * Hq + h * G + g0 + gid) * D + 8 * tig;
 #pragma unroll
-    for (int e = 0; e < E; ++e) part = fmaf(qv[e], k[e], part);
-    const float z = group_sum<LPK>(part) * tau;
-    if (r < n_keys) a.add(z, v);
+    for (int i = 0; i < NV; ++i) {
+      const uint4 y = have ? __ldg(reinterpret_cast<const uint4*>(qr + 32 * i)) : make_uint4(0, 0, 0, 0);
+      mma16816_bf16(acc, xa[i].x, xb[i].x, xa[i].y, xb[i].y, y.x, y.y);
+      mma16816_bf16(acc, xa[i].z, xb[i].z, xa[i].w, xb[i].w, y.z, y.w);
+    }
+    const int g = g0 + 2 * tig;
+    float* out = ws_scores + (int64_t(b) * Hq + h * G + g) * nc;
+    if (c0 + gid < n_cand) {
+      if (g < G) out[c0 + gid] = tau * (acc[0] + ba);
+      if (g + 1 < G) out[nc + c0 + gid] = tau * (acc[1] + ba);
+    }
+    if (c0 + gid + 8 < n_cand) {
+      if (g < G) out[c0 + gid + 8] = tau * (acc[2] + bb);
+      if (g + 1 < G) out[nc + c0 + gid + 8] = tau * (acc[3] + bb);
+    }
   }
+}
+
+// ---------------------------------------------------------------- Q2
+// The K largest scores of a row by bisection of the K-th largest order key:
+// count the keys at or above a threshold until exactly K are, or the interval
+// closes on a tied value, whose lowest ids are taken.  A count costs a few
+// instructions per key and one barrier, and the exit comes after about
+// log2(key range / gap at the K-th score) steps, ten or so; a radix select
+// instead sends all of a row's scores, which share their high bits, through
+// atomics on a few shared counters.  Each thread holds a contiguous segment of
+// keys in registers (IT = 0: re-read from L2), so the ids come out ascending.
+template <int IT>
+__global__ void __launch_bounds__(256)
+quant_topk_kernel(const float* __restrict__ ws_scores, const int32_t* __restrict__ seqlens, int64_t cap, int64_t nc,
+                  int Hq, int K, int32_t* __restrict__ sel_ids, float* __restrict__ sel_scores,
+                  int32_t* __restrict__ ids_out, float* __restrict__ scores_out, int wm1) {
+  __shared__ __align__(16) uint32_t s_part[2][8];
+  __shared__ uint32_t s_min[8], s_max[8];
+  __shared__ int warp_tot[8];
+  pdl_wait();      // the scores
+  pdl_trigger();
+  const int row = blockIdx.x, b = row / Hq, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t own = decode_own_chunk(seqlens, b, cap);
+  int64_t n = own < 0 ? 0 : own - wm1;   // candidates
+  if (n < 0) n = 0;
+  const float* sc = ws_scores + int64_t(row) * nc;
+  const int64_t at = int64_t(row) * K;
+  auto put = [&](int slot, int32_t id, float s) {
+    sel_ids[at + slot] = id;
+    sel_scores[at + slot] = s;
+    if (ids_out) ids_out[at + slot] = id;
+    if (scores_out) scores_out[at + slot] = s;
+  };
+  if (n <= K) {
+    for (int t = tid; t < K; t += 256) put(t, t < n ? t : -1, t < n ? sc[t] : -INFINITY);
+    return;
+  }
+  const int64_t seg = IT > 0 && IT % 4 == 0 ? ((n + 255) / 256 + 3) / 4 * 4 : (n + 255) / 256;
+  const int64_t s0 = tid * seg;
+  const int64_t cnt = s0 >= n ? 0 : (s0 + seg <= n ? seg : n - s0);
+  constexpr int R = IT > 0 ? IT : 1;
+  uint32_t key[R];
+  if constexpr (IT > 0) {
+    // rows of scores start 256-byte aligned when nc is a multiple of 64, else
+    // at any multiple of 4 bytes
+    const bool vec = (nc & 3) == 0;
 #pragma unroll
-  for (int o = LPK; o < 32; o <<= 1) a.merge_xor(o);
-  if (grp != 0) return;
-  const float inv = 1.f / a.l;
+    for (int e = 0; e < IT; e += 4) {
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (vec && e + 4 <= cnt) {
+        v = *reinterpret_cast<const float4*>(sc + s0 + e);
+      } else {
+        if (e < cnt) v.x = sc[s0 + e];
+        if (e + 1 < cnt) v.y = sc[s0 + e + 1];
+        if (e + 2 < cnt) v.z = sc[s0 + e + 2];
+        if (e + 3 < cnt) v.w = sc[s0 + e + 3];
+      }
+      // key 0, which no score has (it is the image of a negative NaN of all
+      // ones), marks the places behind the end
+      key[e] = e < cnt ? max(order_key(v.x), 1u) : 0u;
+      key[e + 1] = e + 1 < cnt ? max(order_key(v.y), 1u) : 0u;
+      key[e + 2] = e + 2 < cnt ? max(order_key(v.z), 1u) : 0u;
+      key[e + 3] = e + 3 < cnt ? max(order_key(v.w), 1u) : 0u;
+    }
+  }
+  auto for_keys = [&](auto f) {   // over this thread's keys, order free
+    if constexpr (IT > 0) {
 #pragma unroll
-  for (int e = 0; e < E; ++e) part_o[(row * PS + slot) * D + sub * E + e] = a.acc[e] * inv;
-  if (sub == 0) part_u[row * PS + slot] = slot >= K ? a.m + logf(a.l) : sel_scores[row * K + slot];
+      for (int e = 0; e < IT; ++e) f(key[e]);
+    } else {
+      for (int64_t c = tid; c < n; c += 256) f(max(order_key(sc[c]), 1u));
+    }
+  };
+  uint32_t lo = 0xFFFFFFFFu, hi = 0u;
+  for_keys([&](uint32_t k) {
+    if (k) lo = min(lo, k);
+    hi = max(hi, k);
+  });
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  if (lane == 0) { s_min[warp] = lo; s_max[warp] = hi; }
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 8; ++w) { lo = min(lo, s_min[w]); hi = max(hi, s_max[w]); }
+  int flip = 0;
+  auto count = [&](uint32_t t) {   // keys >= t of the whole row
+    uint32_t x = 0;
+    for_keys([&](uint32_t k) { x += k >= t; });
+    x = __reduce_add_sync(0xffffffffu, x);
+    if (lane == 0) s_part[flip][warp] = x;
+    __syncthreads();
+    const uint4 p0 = *reinterpret_cast<const uint4*>(s_part[flip]), p1 = *reinterpret_cast<const uint4*>(s_part[flip] + 4);
+    flip ^= 1;
+    return int(p0.x + p0.y + p0.z + p0.w + p1.x + p1.y + p1.z + p1.w);
+  };
+  // the largest t with at least K keys >= t, or any t with exactly K
+  bool exact = false;
+  while (lo < hi) {
+    const uint32_t d = hi - lo, mid = lo + (d >> 1) + (d & 1);
+    const int c = count(mid);
+    if (c >= K) lo = mid; else hi = mid - 1;
+    if (c == K) { exact = true; break; }
+  }
+  const int ties = exact || lo == 0xFFFFFFFFu ? K : K - count(lo + 1);   // how many keys equal to lo are kept
+  // each thread's keys above lo, and equal to it, in chunk order
+  int gt = 0, eq = 0;
+  auto at_key = [&](int64_t e) { return IT > 0 ? 0u : max(order_key(sc[s0 + e]), 1u); };
+  if constexpr (IT > 0) {
+#pragma unroll
+    for (int e = 0; e < IT; ++e) { gt += key[e] > lo; eq += key[e] == lo; }
+  } else {
+    for (int64_t e = 0; e < cnt; ++e) { const uint32_t k = at_key(e); gt += k > lo; eq += k == lo; }
+  }
+  int tot;
+  int take_eq = eq;
+  if (!exact) {
+    take_eq = ties - block_exclusive_scan256(eq, warp_tot, tot);
+    take_eq = take_eq < 0 ? 0 : (take_eq > eq ? eq : take_eq);
+  }
+  int pos = block_exclusive_scan256(gt + take_eq, warp_tot, tot);
+  auto emit = [&](int64_t e, uint32_t k) {
+    bool take = k > lo;
+    if (k == lo) take = take_eq-- > 0;
+    if (take && pos < K) { put(pos, int32_t(s0 + e), sc[s0 + e]); ++pos; }
+  };
+  if (gt + take_eq == 0) return;
+  if constexpr (IT > 0) {
+#pragma unroll
+    for (int e = 0; e < IT; ++e)
+      if (key[e] >= lo && e < cnt) emit(e, key[e]);
+  } else {
+    for (int64_t e = 0; e < cnt; ++e) emit(e, at_key(e));
+  }
+}
+
+// ---------------------------------------------------------------- Q3
+// A cluster of CTAs serves the (up to eight) query heads `oct` of one kv head:
+// its warps share out the distinct chunks that any of these heads kept, and the
+// window's chunks.  A warp stages a chunk's two 4-bit blocks in its own shared
+// memory (copies of the next chunk's keys start as soon as the current ones
+// are consumed, its values likewise) and attends it for all heads that kept
+// it at once:
+//   logits (keys x heads): codes are widened to bf16 16 + code (one shift and
+//     one and-or per two codes), multiplied on the tensor cores with the bf16
+//     queries and summed in fp32 per group of 32 dims, exactly; then
+//     z = tau sum_g [ s_jg acc_jg + (m_jg - 16 s_jg) sum_{i in g} q_i ].
+//     The offset makes a sum about three times larger: no matter in fp32.
+//   output (dims x heads): the codes as they are, fp16 subnormals code 2^-24,
+//     times fp16(w_j s_jg); and m_jg times fp16(w_j), one instruction for all
+//     groups; w_j = e^(z_j - lse) e^(u - M) carries the fusion weight.  Rounding
+//     the weights to fp16 costs 2^-12 of each, an eighth of a bf16 output's.
+// fp32 models: queries, and the weights times s and m, as sums of three bf16
+// values (24 bits), so that the products are fp32's.
+// Running maximum, sum and outputs stay in registers over a warp's chunks;
+// warps merge in shared memory, CTAs through distributed shared memory.
+constexpr int kQdWarps = 8;
+
+template <int D> struct QuantAttend {
+  static constexpr int BLOCK = int(QuantPage<D>::BLOCK);
+  static constexpr int RS = D + 4;                            // floats per merged row: 16-byte stores of four rows apart
+  static constexpr int MERGE = 8 * RS * 4 + 8 * 2 * 4;        // per warp: 8 rows, then (maximum, sum) of 8 heads
+  static constexpr int STAGE = 2 * BLOCK > MERGE ? 2 * BLOCK : (MERGE + 15) / 16 * 16;
+  static constexpr int LISTS = 8 * kMaxTopK;                  // ids, then scores
+  static constexpr int SMEM = kQdWarps * STAGE + MERGE + 2 * LISTS * 4;
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kQdWarps * 32, 2)
+quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, const uint8_t* __restrict__ vpg,
+                    const int32_t* __restrict__ table, int64_t n_pages, const int32_t* __restrict__ seqlens,
+                    int64_t cap, int Hq, int G, int Hkv, int K, float tau, const int32_t* __restrict__ sel_ids,
+                    const float* __restrict__ sel_scores, T* __restrict__ o, int n_oct, int wm1) {
+  using A = QuantAttend<D>;
+  using P = QuantPage<D>;
+  constexpr int NG = P::G, NS = sizeof(T) == 2 ? 1 : 3;
+  constexpr float kLog2e = 1.4426950408889634f;
+  constexpr float OFF = NS == 1 ? 16.f : -8.f;     // what codes_bf16 adds to a code
+  namespace cg = cooperative_groups;
+  extern __shared__ __align__(16) uint8_t qsm[];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gid = lane >> 2, tig = lane & 3;
+  const uint32_t CL = gridDim.x, rank = blockIdx.x;     // the cluster is the grid's row
+  const int oct = blockIdx.y % n_oct, bh = blockIdx.y / n_oct, b = bh / Hkv, h = bh % Hkv;
+  const int g0 = oct * 8, GV = G - g0 < 8 ? G - g0 : 8;
+  const int64_t row0 = int64_t(b) * Hq + int64_t(h) * G + g0;
+  uint8_t* stage = qsm + warp * A::STAGE;
+  float* cta_part = reinterpret_cast<float*>(qsm + kQdWarps * A::STAGE);
+  int32_t* ids = reinterpret_cast<int32_t*>(qsm + kQdWarps * A::STAGE + A::MERGE);
+  float* scs = reinterpret_cast<float*>(ids + A::LISTS);
+  const uint32_t stage_a = uint32_t(__cvta_generic_to_shared(stage));
+
+  // queries as the column operand: head gid, dims 32 g + 8 tig + {i, i + 4} in
+  // register i of group g, the order in which two 16-bit units of codes unpack
+  uint32_t qb[NS][NG][4];
+  float qsum[NG][2];      // sum of the group's q of heads 2 tig, 2 tig + 1
+  {
+    const T* qr = q + (row0 + (gid < GV ? gid : 0)) * D + 8 * tig;
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      float x[8];
+      if constexpr (NS == 1) {
+        Vec16<T>::load(qr + 32 * g, x);
+      } else {
+        float y[4], z[4];
+        Vec16<T>::load(qr + 32 * g, y);
+        Vec16<T>::load(qr + 32 * g + 4, z);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) { x[e] = y[e]; x[e + 4] = z[e]; }
+      }
+      float s = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (gid >= GV) x[e] = 0.f;
+        s += x[e];
+      }
+#pragma unroll
+      for (int n = 0; n < NS; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t r = pack_bf16(x[i], x[i + 4]);
+          qb[n][g][i] = r;
+          x[i] -= lo_bf16(r);
+          x[i + 4] -= hi_bf16(r);
+        }
+      s += __shfl_xor_sync(0xffffffffu, s, 1);
+      s += __shfl_xor_sync(0xffffffffu, s, 2);
+      qsum[g][0] = __shfl_sync(0xffffffffu, s, 8 * tig);
+      qsum[g][1] = __shfl_sync(0xffffffffu, s, 8 * tig + 4);
+    }
+  }
+  const int64_t own = decode_own_chunk(seqlens, b, cap), nc = cap / kChunk;
+  const int n_own = own < 0 ? 0 : int(__ldg(seqlens + b) - own * kChunk);   // keys of the own chunk
+  const int64_t n_cand = own - wm1 > 0 ? own - wm1 : 0;
+  const int n_sel = own < 0 ? 0 : GV * K;
+  const int n_win = own < 0 ? 0 : int(own < wm1 ? own + 1 : wm1 + 1);
+  pdl_wait();      // the top-K lists
+  for (int i = tid; i < n_sel; i += kQdWarps * 32) {
+    ids[i] = sel_ids[row0 * K + i];
+    scs[i] = sel_scores[row0 * K + i];
+  }
+  __syncthreads();
+
+  // the next slot of this warp at or after s whose chunk is its to attend
+  struct Work {
+    int slot;          // -1: none left
+    uint32_t heads;    // who attends the chunk
+    float u[2];        // their fusion scores x log2 e (heads 2 tig, 2 tig + 1; selected chunks)
+    const uint8_t *k, *v;
+    int keys;
+    bool window;
+  };
+  const int n_slots = n_sel + n_win, step = int(CL) * kQdWarps;
+  auto find = [&](int s) {
+    Work w{-1, 0u, {0.f, 0.f}, nullptr, nullptr, kChunk, false};
+    for (; s < n_slots; s += step) {
+      int64_t c;
+      float mine = 0.f;
+      if (s >= n_sel) {
+        c = own - (s - n_sel);
+        w.window = true;
+        w.keys = s == n_sel ? n_own : kChunk;
+        w.heads = (1u << GV) - 1u;
+      } else {
+        const int g = s / K;
+        c = ids[s];
+        if (c < 0 || c >= n_cand) {
+          if (c >= 0 && lane == 0) record_error(HILS_ERR_DEVICE_BOUNDS);
+          continue;
+        }
+        bool has = false;
+        if (lane < GV) {
+          int lo = lane * K, hi = lo + K - 1;     // ascending, -1 padding behind
+          while (lo <= hi) {
+            const int mid = (lo + hi) >> 1, v = ids[mid];
+            if (v == c) { has = true; mine = scs[mid] * kLog2e; break; }
+            if (v >= 0 && v < c) lo = mid + 1; else hi = mid - 1;
+          }
+        }
+        w.heads = __ballot_sync(0xffffffffu, has);
+        if (w.heads & ((1u << g) - 1u)) continue;    // an earlier head's slot takes the chunk
+      }
+      int64_t off = 0;
+      if (lane == 0) off = quant_block_offset<D>(table, n_pages, b, h, c, Hkv, nc);
+      off = __shfl_sync(0xffffffffu, off, 0);
+      if (off < 0) { w.window = false; w.keys = kChunk; continue; }
+      w.u[0] = __shfl_sync(0xffffffffu, mine, 2 * tig);
+      w.u[1] = __shfl_sync(0xffffffffu, mine, 2 * tig + 1);
+      w.k = kpg + off;
+      w.v = vpg + off;
+      w.slot = s;
+      return w;
+    }
+    return w;
+  };
+  auto copy = [&](const uint8_t* src, uint32_t dst) {
+#pragma unroll
+    for (int i = 0; i < A::BLOCK / 512; ++i) cp_async16(dst + uint32_t(lane + 32 * i) * 16u, src + (lane + 32 * i) * 16);
+  };
+  auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
+  auto wait_all_but_one = [] { asm volatile("cp.async.wait_group 1;" ::: "memory"); };
+
+  float acc[NG][2][4], least[2] = {0.f, 0.f}, M[2] = {-INFINITY, -INFINITY}, Z[2] = {0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < NG * 8; ++i) acc[i / 8][i / 4 % 2][i % 4] = 0.f;
+
+  Work cur = find(int(rank) + warp * int(CL));
+  if (cur.slot >= 0) copy(cur.k, stage_a);
+  commit();
+  if (cur.slot >= 0) copy(cur.v, stage_a + A::BLOCK);
+  commit();
+  while (cur.slot >= 0) {
+    const Work nxt = find(cur.slot + step);
+    wait_all_but_one();
+    __syncwarp();
+    // ---- logits: tile t, rows are keys 16 t + gid and + 8, columns heads 2 tig, 2 tig + 1
+    float z[4][4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      uint32_t cw[2][NG];      // the lane's two units of each group, one register each, for the two rows
+      float ps[2][NG], pm[2][NG];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int key = 16 * t + 8 * r + gid;
+        if constexpr (NG == 4) {
+          const uint4 u = *reinterpret_cast<const uint4*>(stage + P::code_off(key) + 16 * tig);
+          cw[r][0] = __byte_perm(u.x, u.z, 0x5410);
+          cw[r][1] = __byte_perm(u.x, u.z, 0x7632);
+          cw[r][2] = __byte_perm(u.y, u.w, 0x5410);
+          cw[r][3] = __byte_perm(u.y, u.w, 0x7632);
+        } else {
+          const uint2 u = *reinterpret_cast<const uint2*>(stage + P::code_off(key) + 8 * tig);
+          cw[r][0] = __byte_perm(u.x, u.y, 0x5410);
+          cw[r][1] = __byte_perm(u.x, u.y, 0x7632);
+        }
+        const __half2* par = reinterpret_cast<const __half2*>(stage + P::param_off(key));
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          const float2 sm = __half22float2(par[g]);
+          ps[r][g] = sm.x;
+          pm[r][g] = fmaf(-OFF, sm.x, sm.y);
+        }
+      }
+      z[t][0] = z[t][1] = z[t][2] = z[t][3] = 0.f;
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        uint32_t a[2][4];
+        codes_bf16<NS == 3>(cw[0][g], a[0]);
+        codes_bf16<NS == 3>(cw[1][g], a[1]);
+        float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int n = NS - 1; n >= 0; --n) {
+          mma16816_bf16(c, a[0][0], a[1][0], a[0][1], a[1][1], qb[n][g][0], qb[n][g][1]);
+          mma16816_bf16(c, a[0][2], a[1][2], a[0][3], a[1][3], qb[n][g][2], qb[n][g][3]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z[t][i] = fmaf(ps[i / 2][g], c[i], fmaf(pm[i / 2][g], qsum[g][i % 2], z[t][i]));
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        z[t][i] *= tau * kLog2e;
+        if (16 * t + 8 * (i / 2) + gid >= cur.keys) z[t][i] = -INFINITY;
+      }
+    }
+    __syncwarp();
+    if (nxt.slot >= 0) copy(nxt.k, stage_a);
+    commit();
+    // ---- the chunk's softmax and its place in the fusion
+    float coef[2], alpha[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float m = -INFINITY, l = 0.f;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) m = fmaxf(m, fmaxf(z[t][e], z[t][2 + e]));
+#pragma unroll
+      for (int x = 4; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        z[t][e] = exp2f(z[t][e] - m);
+        z[t][2 + e] = exp2f(z[t][2 + e] - m);
+        l += z[t][e] + z[t][2 + e];
+      }
+#pragma unroll
+      for (int x = 4; x < 32; x <<= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+      const bool kept = (cur.heads >> (2 * tig + e)) & 1u;
+      const float u = cur.window ? m + log2f(l) : cur.u[e];
+      const float mn = kept ? fmaxf(M[e], u) : M[e];
+      alpha[e] = mn == -INFINITY ? 1.f : exp2f(M[e] - mn);
+      const float beta = kept && mn != -INFINITY ? exp2f(u - mn) : 0.f;
+      Z[e] = fmaf(Z[e], alpha[e], beta);
+      coef[e] = kept ? beta / l : 0.f;
+      M[e] = mn;
+    }
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[g][i / 4][i % 4] *= alpha[i & 1];
+    least[0] *= alpha[0];
+    least[1] *= alpha[1];
+    wait_all_but_one();
+    __syncwarp();
+    // ---- output
+    const uint8_t* vst = stage + A::BLOCK;
+    float lm[4] = {0.f, 0.f, 0.f, 0.f};      // the chunk's least values, one row per group
+    const uint32_t kept_mask = (cur.heads >> gid) & 1u ? 0xFFFFFFFFu : 0u;   // of the column this lane feeds
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      // the weights with heads as columns: keys 16 t + 2 tig + {0, 1} and + 8 of head gid
+      uint32_t wb[2];        // fp16 pairs
+      float wf[2][2];        // or fp32
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float w0 = z[t][2 * r] * coef[0], w1 = z[t][2 * r + 1] * coef[1];
+        if constexpr (NS == 1) {
+          wb[r] = movmatrix(pack_f16(w0, w1)) & kept_mask;
+        } else {
+          const uint32_t lo = movmatrix(__byte_perm(__float_as_uint(w0), __float_as_uint(w1), 0x5410)) & kept_mask;
+          const uint32_t hi = movmatrix(__byte_perm(__float_as_uint(w0), __float_as_uint(w1), 0x7632)) & kept_mask;
+          wf[r][0] = __uint_as_float(__byte_perm(lo, hi, 0x5410));
+          wf[r][1] = __uint_as_float(__byte_perm(lo, hi, 0x7632));
+        }
+      }
+      uint32_t vc[2][2][NG / 2], vp[2][2][NG];    // codes and parameters of key 16 t + 8 r + 2 tig + j
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int key = 16 * t + 8 * r + 2 * tig + j;
+          const bool in = key < cur.keys;     // parameters behind the sequence may be anything
+          if constexpr (NG == 4) {
+            const uint2 u = *reinterpret_cast<const uint2*>(vst + P::code_off(key) + 8 * gid);
+            vc[r][j][0] = u.x;
+            vc[r][j][1] = u.y;
+            const uint4 p = *reinterpret_cast<const uint4*>(vst + P::param_off(key));
+            vp[r][j][0] = in ? p.x : 0u;
+            vp[r][j][1] = in ? p.y : 0u;
+            vp[r][j][2] = in ? p.z : 0u;
+            vp[r][j][3] = in ? p.w : 0u;
+          } else {
+            vc[r][j][0] = *reinterpret_cast<const uint32_t*>(vst + P::code_off(key) + 4 * gid);
+            const uint2 p = *reinterpret_cast<const uint2*>(vst + P::param_off(key));
+            vp[r][j][0] = in ? p.x : 0u;
+            vp[r][j][1] = in ? p.y : 0u;
+          }
+        }
+      if constexpr (NS == 1) {
+        // least values of group gid as the rows of one product with the weights
+        uint32_t la[2] = {0u, 0u};
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+          if (gid == g) {
+            la[0] = __byte_perm(vp[0][0][g], vp[0][1][g], 0x7632);
+            la[1] = __byte_perm(vp[1][0][g], vp[1][1][g], 0x7632);
+          }
+        mma16816_f16(lm, la[0], 0u, la[1], 0u, wb[0], wb[1]);
+      }
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        uint32_t x[2];       // units of the two keys of each half side by side
+#pragma unroll
+        for (int r = 0; r < 2; ++r) x[r] = __byte_perm(vc[r][0][g / 2], vc[r][1][g / 2], g & 1 ? 0x7632 : 0x5410);
+        if constexpr (NS == 1) {
+          uint32_t bs[2];
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const uint32_t s2 = __byte_perm(vp[r][0][g], vp[r][1][g], 0x5410);
+            const __half2 ws = __hmul2(*reinterpret_cast<const __half2*>(&wb[r]), *reinterpret_cast<const __half2*>(&s2));
+            bs[r] = *reinterpret_cast<const uint32_t*>(&ws) & kept_mask;
+          }
+          mma16816_f16(acc[g][0], x[0] & 0x000F000Fu, (x[0] >> 4) & 0x000F000Fu, x[1] & 0x000F000Fu,
+                       (x[1] >> 4) & 0x000F000Fu, bs[0], bs[1]);
+          mma16816_f16(acc[g][1], (x[0] >> 8) & 0x000F000Fu, (x[0] >> 12) & 0x000F000Fu, (x[1] >> 8) & 0x000F000Fu,
+                       (x[1] >> 12) & 0x000F000Fu, bs[0], bs[1]);
+        } else {
+          // w s and w (m + 8 s) as sums of three bf16 values, the latter through
+          // rows of ones
+          float fs[2][2], fm[2][2];
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float2 sm = __half22float2(*reinterpret_cast<const __half2*>(&vp[r][j][g]));
+              fs[r][j] = kept_mask ? wf[r][j] * sm.x : 0.f;
+              fm[r][j] = kept_mask ? wf[r][j] * fmaf(-OFF, sm.x, sm.y) : 0.f;
+            }
+          uint32_t a[2][4];
+          codes_bf16<true>(x[0], a[0]);
+          codes_bf16<true>(x[1], a[1]);
+          // fresh sums per tile, added in fp32: the matrix unit's own sums are not rounded to nearest
+          float c0[4] = {0.f, 0.f, 0.f, 0.f}, c1[4] = {0.f, 0.f, 0.f, 0.f}, cm[4] = {0.f, 0.f, 0.f, 0.f};
+          constexpr uint32_t one = 0x3F803F80u;
+#pragma unroll
+          for (int n = 0; n < 3; ++n) {
+            const uint32_t s0 = pack_bf16(fs[0][0], fs[0][1]), s1 = pack_bf16(fs[1][0], fs[1][1]);
+            const uint32_t m0 = pack_bf16(fm[0][0], fm[0][1]), m1 = pack_bf16(fm[1][0], fm[1][1]);
+            mma16816_bf16(c0, a[0][0], a[0][1], a[1][0], a[1][1], s0, s1);
+            mma16816_bf16(c1, a[0][2], a[0][3], a[1][2], a[1][3], s0, s1);
+            mma16816_bf16(cm, one, one, one, one, m0, m1);
+            fs[0][0] -= lo_bf16(s0); fs[0][1] -= hi_bf16(s0); fs[1][0] -= lo_bf16(s1); fs[1][1] -= hi_bf16(s1);
+            fm[0][0] -= lo_bf16(m0); fm[0][1] -= hi_bf16(m0); fm[1][0] -= lo_bf16(m1); fm[1][1] -= hi_bf16(m1);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            acc[g][0][i] += c0[i] + cm[i];
+            acc[g][1][i] += c1[i] + cm[i];
+          }
+        }
+      }
+    }
+    // a NaN among the least values is the kept heads' alone (0 x NaN in the other columns)
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      if ((cur.heads >> (2 * tig + e)) & 1u) least[e] += lm[e];
+    __syncwarp();
+    if (nxt.slot >= 0) copy(nxt.v, stage_a + A::BLOCK);
+    commit();
+    cur = nxt;
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncwarp();
+
+  // ---- the warp's sums to its stage: row per head, then (maximum, sum)
+  float* mine = reinterpret_cast<float*>(stage);
+#pragma unroll
+  for (int g = 0; g < NG; ++g)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float add = 0.f, f = 1.f;
+      if constexpr (NS == 1) {
+        add = __shfl_sync(0xffffffffu, least[e], 4 * g + tig);
+        f = 16777216.f;      // the codes were multiplied as code 2^-24
+      }
+      // dims 32 g + 4 gid + 0 .. 3
+      *reinterpret_cast<float4*>(mine + (2 * tig + e) * A::RS + 32 * g + 4 * gid) =
+          make_float4(fmaf(acc[g][0][e], f, add), fmaf(acc[g][0][2 + e], f, add), fmaf(acc[g][1][e], f, add),
+                      fmaf(acc[g][1][2 + e], f, add));
+    }
+  if (gid == 0)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      mine[8 * A::RS + 2 * (2 * tig + e)] = M[e];
+      mine[8 * A::RS + 2 * (2 * tig + e) + 1] = Z[e];
+    }
+  __syncthreads();
+  // ---- warps to the CTA's sums
+  constexpr int WS = A::STAGE / 4;
+  const float* all = reinterpret_cast<const float*>(qsm);
+  for (int i = tid; i < GV * D; i += kQdWarps * 32) {
+    const int g = i / D, t = i % D;
+    float m = -INFINITY, s = 0.f, zz = 0.f;
+#pragma unroll
+    for (int w = 0; w < kQdWarps; ++w) m = fmaxf(m, all[w * WS + 8 * A::RS + 2 * g]);
+#pragma unroll
+    for (int w = 0; w < kQdWarps; ++w) {
+      const float mw = all[w * WS + 8 * A::RS + 2 * g];
+      if (mw == -INFINITY) continue;       // attended nothing for this head
+      const float f = exp2f(mw - m);
+      s = fmaf(f, all[w * WS + g * A::RS + t], s);
+      zz = fmaf(f, all[w * WS + 8 * A::RS + 2 * g + 1], zz);
+    }
+    cta_part[g * A::RS + t] = s;
+    if (t == 0) {
+      cta_part[8 * A::RS + 2 * g] = m;
+      cta_part[8 * A::RS + 2 * g + 1] = zz;
+    }
+  }
+  // ---- CTAs to the output: CTA `rank` finishes heads rank, rank + CL, ...
+  cg::cluster_group cluster = cg::this_cluster();
+  cluster.sync();
+  for (int g = int(rank); g < GV; g += int(CL)) {
+    for (int t = tid; t < D; t += kQdWarps * 32) {
+      float m = -INFINITY, s = 0.f, zz = 0.f;
+      for (uint32_t c = 0; c < CL; ++c) m = fmaxf(m, cluster.map_shared_rank(cta_part, c)[8 * A::RS + 2 * g]);
+      for (uint32_t c = 0; c < CL; ++c) {
+        const float* part = cluster.map_shared_rank(cta_part, c);
+        const float mc = part[8 * A::RS + 2 * g];
+        if (mc == -INFINITY) continue;
+        const float f = exp2f(mc - m);
+        s = fmaf(f, part[g * A::RS + t], s);
+        zz = fmaf(f, part[8 * A::RS + 2 * g + 1], zz);
+      }
+      const float y = zz != 0.f ? s / zz : 0.f;       // nothing attended: 0
+      T* out = o + (row0 + g) * D + t;
+      if constexpr (NS == 1) *out = __float2bfloat16_rn(y);
+      else *out = y;
+    }
+  }
+  cluster.sync();      // no CTA leaves while its sums are read
 }
 
 }  // namespace hils

@@ -964,6 +964,23 @@ int summary_append_entry(const hils_dims* d, const hils_tokens* tk, const void* 
   }
 }
 
+struct QuantWs {
+  float* scores;      // [B*Hq, nc]
+  int32_t* ids;       // [B*Hq, K]
+  float* sel;         // [B*Hq, K]
+};
+
+size_t quant_ws_layout(const hils_dims* d, char* base, QuantWs* ws) {
+  const size_t rows = size_t(d->batch) * d->heads_q;
+  size_t off = 0;
+  auto take = [&](size_t bytes) { char* p = base ? base + off : nullptr; off += align256(bytes); return p; };
+  char* a = take(sizeof(float) * rows * size_t(d->seqlen / kChunk));
+  char* b = take(sizeof(int32_t) * rows * d->topk);
+  char* c = take(sizeof(float) * rows * d->topk);
+  if (ws) *ws = QuantWs{reinterpret_cast<float*>(a), reinterpret_cast<int32_t*>(b), reinterpret_cast<float*>(c)};
+  return off;
+}
+
 template <typename T, int D>
 int launch_decode_quant(const hils_dims* d, const void* q, const void* q_score, const void* kpg, const void* vpg,
                         const int32_t* table, int64_t n_pages, const float* kp, const float* bp, const void* kmma,
@@ -971,33 +988,58 @@ int launch_decode_quant(const hils_dims* d, const void* q, const void* q_score, 
                         cudaStream_t st) {
   constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
   const int64_t nc = d->seqlen / kChunk, rows = int64_t(d->batch) * d->heads_q;
-  const int G = d->heads_q / d->heads_kv, K = d->topk, wm1 = window_wm1(d), PS = K + wm1 + 1;
+  const int G = d->heads_q / d->heads_kv, K = d->topk, wm1 = window_wm1(d);
   const float tau = 1.f / sqrtf(float(D));
-  DecodeWs ws;
-  decode_ws_layout(rows, nc, K, wm1 + 1, D, static_cast<char*>(ws_ptr), &ws);
-  const size_t smem1 = decode_scores_smem<D, BF>(G);
-  constexpr auto k1 = decode_scores_kernel<T, D, BF>;
-  if (smem1 > 48 * 1024 && set_smem_max<k1>() != cudaSuccess) return HILS_ERR_CUDA;
-  dim3 g1(unsigned((nc + kDecChunksPerCta - 1) / kDecChunksPerCta), unsigned(d->batch * d->heads_kv));
-  k1<<<g1, kDecChunksPerCta, smem1, st>>>(static_cast<const T*>(q_score ? q_score : q), kp, bp,
-                                          static_cast<const __nv_bfloat16*>(kmma), seqlens, d->seqlen, nc, d->heads_q,
-                                          G, d->heads_kv, tau, ws.scores, wm1);
-  cudaError_t e = launch_pdl(decode_topk_kernel, dim3(unsigned(rows)), 256, 0, st, ws.scores, seqlens, d->seqlen, nc,
-                             d->heads_q, K, ws.sel_ids, ws.sel_scores, wm1);
+  QuantWs ws;
+  quant_ws_layout(d, static_cast<char*>(ws_ptr), &ws);
+  const T* qs = static_cast<const T*>(q_score ? q_score : q);
+  const unsigned bh = unsigned(d->batch * d->heads_kv);
+  if constexpr (BF) {
+    quant_scores_kernel<D><<<dim3(unsigned((nc + 63) / 64), bh), 128, 0, st>>>(
+        qs, static_cast<const __nv_bfloat16*>(kmma), seqlens, d->seqlen, nc, d->heads_q, G, d->heads_kv, tau, ws.scores,
+        wm1);
+  } else {
+    const size_t smem1 = decode_scores_smem<D, BF>(G);
+    decode_scores_kernel<T, D, BF><<<dim3(unsigned((nc + kDecChunksPerCta - 1) / kDecChunksPerCta), bh),
+                                     kDecChunksPerCta, smem1, st>>>(qs, kp, bp, nullptr, seqlens, d->seqlen, nc,
+                                                                    d->heads_q, G, d->heads_kv, tau, ws.scores, wm1);
+  }
+  auto topk = [&](auto* fn) {
+    return launch_pdl(fn, dim3(unsigned(rows)), 256, 0, st, static_cast<const float*>(ws.scores), seqlens, d->seqlen, nc,
+                      d->heads_q, K, ws.ids, ws.sel, ids_out, scores_out, wm1);
+  };
+  cudaError_t e = nc <= 256 * 8    ? topk(quant_topk_kernel<8>)
+                  : nc <= 256 * 32 ? topk(quant_topk_kernel<32>)
+                  : nc <= 256 * 96 ? topk(quant_topk_kernel<96>)
+                                   : topk(quant_topk_kernel<0>);
   if (e != cudaSuccess) return HILS_ERR_CUDA;
-  const int64_t items = rows * PS;
-  e = launch_pdl(decode_partial_quant_kernel<T, D>, dim3(unsigned((items + 3) / 4)), 128, 0, st,
-                 static_cast<const T*>(q), static_cast<const uint8_t*>(kpg), static_cast<const uint8_t*>(vpg), table,
-                 n_pages, seqlens, d->seqlen, d->heads_q, G, d->heads_kv, K, tau,
-                 static_cast<const int32_t*>(ws.sel_ids), static_cast<const float*>(ws.sel_scores), ws.part_u,
-                 ws.part_o, items, wm1);
+  constexpr auto k3 = quant_attend_kernel<T, D>;
+  if (set_smem_max<k3>() != cudaSuccess) return HILS_ERR_CUDA;
+  // CTAs per cluster: enough for every warp to have a chunk, no more than
+  // fill the GPU twice over
+  const int n_oct = (G + 7) / 8, heads = G < 8 ? G : 8;
+  const int64_t groups = int64_t(bh) * n_oct, slots = int64_t(heads) * K + wm1 + 1;
+  unsigned cl = 1;
+  while (cl < 8 && int64_t(cl) * kQdWarps < slots && groups * cl < 2 * sm_count()) cl *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(cl, unsigned(groups));
+  cfg.blockDim = dim3(kQdWarps * 32);
+  cfg.dynamicSmemBytes = QuantAttend<D>::SMEM;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cl;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, k3, static_cast<const T*>(q), static_cast<const uint8_t*>(kpg),
+                         static_cast<const uint8_t*>(vpg), table, n_pages, seqlens, d->seqlen, int(d->heads_q), G,
+                         int(d->heads_kv), K, tau, static_cast<const int32_t*>(ws.ids), static_cast<const float*>(ws.sel),
+                         static_cast<T*>(o), n_oct, wm1);
   if (e != cudaSuccess) return HILS_ERR_CUDA;
-  e = launch_pdl(decode_combine_kernel<T, D>, dim3(unsigned(rows)), D, 0, st,
-                 static_cast<const float*>(ws.part_u), static_cast<const float*>(ws.part_o), seqlens, d->seqlen,
-                 d->heads_q, K, static_cast<const int32_t*>(ws.sel_ids), static_cast<const float*>(ws.sel_scores),
-                 static_cast<T*>(o), ids_out, scores_out, rows, wm1);
-  if (e != cudaSuccess) return HILS_ERR_CUDA;
-  return launched(4);
+  return launched(3);
 }
 
 }  // namespace
@@ -1065,7 +1107,9 @@ int hils_landmark_summary_quant(const hils_dims* d, const hils_tokens* tokens, c
   return summary_append_entry<true>(d, tokens, k_pages, page_table, n_pages, lq, kprime, bprime, kprime_mma, stream);
 }
 
-size_t hils_decode_quant_workspace_bytes(const hils_dims* d) { return hils_decode_workspace_bytes(d); }
+size_t hils_decode_quant_workspace_bytes(const hils_dims* d) {
+  return check_dims(d) == HILS_OK ? quant_ws_layout(d, nullptr, nullptr) : 0;
+}
 
 int hils_attn_decode_quant(const hils_dims* d, const void* q, const void* q_score, const void* k_pages,
                            const void* v_pages, const int32_t* page_table, int64_t n_pages, const float* kprime,
@@ -1075,7 +1119,8 @@ int hils_attn_decode_quant(const hils_dims* d, const void* q, const void* q_scor
   int rc = check_dims(d);
   if (rc) return rc;
   if (d->heads_q / d->heads_kv > 32) return HILS_ERR_UNSUPPORTED;
-  if (int64_t(d->batch) * d->heads_kv > 65535) return HILS_ERR_UNSUPPORTED;   // the scoring grid's second dimension
+  // the grids' second dimension: a (sequence, kv head, eight query heads) each
+  if (int64_t(d->batch) * d->heads_kv * ((d->heads_q / d->heads_kv + 7) / 8) > 65535) return HILS_ERR_UNSUPPORTED;
   if (!ptr_ok(q) || !aligned16(q_score) || !ptr_ok(k_pages) || !ptr_ok(v_pages) || !ptr_ok(page_table) ||
       n_pages < 1 || !ptr_ok(seqlens) || !ptr_ok(o) || !aligned16(ids_out) || !aligned16(scores_out))
     return HILS_ERR_INVALID_ARGUMENT;

@@ -219,7 +219,8 @@ class _Loop:
             t.zero_()
         self.seqlens = torch.zeros(B, dtype=torch.int32, device="cuda")
         self.new = torch.empty((B, Hq + 2 * Hkv, d), dtype=torch.bfloat16, device="cuda")
-        self.ws = torch.empty((hils.hils_decode_quant_workspace_bytes(self.dims),), dtype=torch.uint8, device="cuda")
+        need = hils.hils_decode_quant_workspace_bytes if quant else hils.hils_decode_workspace_bytes
+        self.ws = torch.empty((need(self.dims),), dtype=torch.uint8, device="cuda")
         self.o = torch.empty((B, Hq, d), dtype=torch.bfloat16, device="cuda")
 
     def _split(self, x):
