@@ -43,6 +43,15 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 __device__ __forceinline__ float lo_bf16(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float hi_bf16(uint32_t x) { return __uint_as_float(x & 0xFFFF0000u); }
 
+// 2^x.  FAST: without the scaling that keeps results below 2^-126 (weights that small are zero here)
+template <bool FAST>
+__device__ __forceinline__ float pow2(float x) {
+  if constexpr (!FAST) return exp2f(x);
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // Four codes of two 16-bit units as bf16 pairs: 16 + code has the code in
 // bits 3 .. 6.  CENTRE: code - 8 instead, exactly (one subtraction more; the
 // products' sums then do not carry the offset, which fp32 results would feel).
@@ -262,9 +271,9 @@ quant_topk_kernel(const float* __restrict__ ws_scores, const int32_t* __restrict
 // it at once:
 //   logits (keys x heads): codes are widened to bf16 16 + code (one shift and
 //     one and-or per two codes), multiplied on the tensor cores with the bf16
-//     queries and summed in fp32 per group of 32 dims, exactly; then
-//     z = tau sum_g [ s_jg acc_jg + (m_jg - 16 s_jg) sum_{i in g} q_i ].
-//     The offset makes a sum about three times larger: no matter in fp32.
+//     queries and summed in fp32 per group of 32 dims, starting from -16 times
+//     the group's sum of q, so that acc_jg = sum_{i in g} q_i code_ji; then
+//     z = tau sum_g [ s_jg acc_jg + m_jg sum_{i in g} q_i ].
 //   output (dims x heads): the codes as they are, fp16 subnormals code 2^-24,
 //     times fp16(w_j s_jg); and m_jg times fp16(w_j), one instruction for all
 //     groups; w_j = e^(z_j - lse) e^(u - M) carries the fusion weight.  Rounding
@@ -280,8 +289,11 @@ template <int D> struct QuantAttend {
   static constexpr int RS = D + 4;                            // floats per merged row: 16-byte stores of four rows apart
   static constexpr int MERGE = 8 * RS * 4 + 8 * 2 * 4;        // per warp: 8 rows, then (maximum, sum) of 8 heads
   static constexpr int STAGE = 2 * BLOCK > MERGE ? 2 * BLOCK : (MERGE + 15) / 16 * 16;
-  static constexpr int LISTS = 8 * kMaxTopK;                  // ids, then scores
-  static constexpr int SMEM = kQdWarps * STAGE + MERGE + 2 * LISTS * 4;
+  static constexpr int LISTS = 8 * kMaxTopK;                  // kept (head, slot) pairs of a cluster, at most
+  static constexpr int ITEMS = LISTS + 16;                    // distinct chunks and window chunks
+  // staging, the CTA's sums, scores of the pairs, places of a pair's chunk in
+  // the heads' lists, ids of the pairs, then the items' page and pair
+  static constexpr int SMEM = kQdWarps * STAGE + MERGE + LISTS * 4 + LISTS * 8 + LISTS * 4 + ITEMS * 8;
 };
 
 template <typename T, int D>
@@ -295,6 +307,7 @@ quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, co
   constexpr int NG = P::G, NS = sizeof(T) == 2 ? 1 : 3;
   constexpr float kLog2e = 1.4426950408889634f;
   constexpr float OFF = NS == 1 ? 16.f : -8.f;     // what codes_bf16 adds to a code
+  constexpr float kSumScale = 1.f / 256.f;         // of the sums of q in fp16: |q| up to 5e5
   namespace cg = cooperative_groups;
   extern __shared__ __align__(16) uint8_t qsm[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gid = lane >> 2, tig = lane & 3;
@@ -304,14 +317,18 @@ quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, co
   const int64_t row0 = int64_t(b) * Hq + int64_t(h) * G + g0;
   uint8_t* stage = qsm + warp * A::STAGE;
   float* cta_part = reinterpret_cast<float*>(qsm + kQdWarps * A::STAGE);
-  int32_t* ids = reinterpret_cast<int32_t*>(qsm + kQdWarps * A::STAGE + A::MERGE);
-  float* scs = reinterpret_cast<float*>(ids + A::LISTS);
+  float* scs = reinterpret_cast<float*>(qsm + kQdWarps * A::STAGE + A::MERGE);     // [GV][K], x log2 e
+  uint8_t* spot = reinterpret_cast<uint8_t*>(scs + A::LISTS);                       // [pair][8 heads]: slot, 0xFF: not kept
+  int32_t* ids = reinterpret_cast<int32_t*>(spot + A::LISTS * 8);                   // [GV][K]
+  int2* items = reinterpret_cast<int2*>(ids + A::LISTS);                            // (page, pair; -1 - w: window chunk w)
+  __shared__ int s_count[kQdWarps];
   const uint32_t stage_a = uint32_t(__cvta_generic_to_shared(stage));
 
   // queries as the column operand: head gid, dims 32 g + 8 tig + {i, i + 4} in
   // register i of group g, the order in which two 16-bit units of codes unpack
   uint32_t qb[NS][NG][4];
-  float qsum[NG][2];      // sum of the group's q of heads 2 tig, 2 tig + 1
+  float qoff[NG][2];      // -OFF x the group's sum of q, heads 2 tig, 2 tig + 1: what the codes' offset adds
+  uint32_t qs2[2] = {0u, 0u};   // NS == 1: the sums as a column operand, see the logits
   {
     const T* qr = q + (row0 + (gid < GV ? gid : 0)) * D + 8 * tig;
 #pragma unroll
@@ -343,8 +360,16 @@ quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, co
         }
       s += __shfl_xor_sync(0xffffffffu, s, 1);
       s += __shfl_xor_sync(0xffffffffu, s, 2);
-      qsum[g][0] = __shfl_sync(0xffffffffu, s, 8 * tig);
-      qsum[g][1] = __shfl_sync(0xffffffffu, s, 8 * tig + 4);
+      qoff[g][0] = -OFF * __shfl_sync(0xffffffffu, s, 8 * tig);
+      qoff[g][1] = -OFF * __shfl_sync(0xffffffffu, s, 8 * tig + 4);
+      if constexpr (NS == 1) {
+        // rows 2 tig, 2 tig + 1 (groups) in fp16, rows + 8 what that rounds off
+        if (g / 2 == tig) {
+          const float v = s * kSumScale, r = v - __half2float(__float2half_rn(v));
+          qs2[0] |= pack_f16(v, 0.f) << (16 * (g % 2));
+          qs2[1] |= pack_f16(r, 0.f) << (16 * (g % 2));
+        }
+      }
     }
   }
   const int64_t own = decode_own_chunk(seqlens, b, cap), nc = cap / kChunk;
@@ -353,62 +378,99 @@ quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, co
   const int n_sel = own < 0 ? 0 : GV * K;
   const int n_win = own < 0 ? 0 : int(own < wm1 ? own + 1 : wm1 + 1);
   pdl_wait();      // the top-K lists
-  for (int i = tid; i < n_sel; i += kQdWarps * 32) {
+  constexpr int TH = kQdWarps * 32;
+  for (int i = tid; i < n_sel; i += TH) {
     ids[i] = sel_ids[row0 * K + i];
-    scs[i] = sel_scores[row0 * K + i];
+    scs[i] = sel_scores[row0 * K + i] * kLog2e;
+  }
+  for (int i = tid; i < n_sel * 2; i += TH) reinterpret_cast<uint32_t*>(spot)[i] = 0xFFFFFFFFu;
+  __syncthreads();
+  // who else kept the chunk of each (head, slot) pair: one lane per (pair,
+  // head), binary search in the head's ascending list (-1 padding behind).  The
+  // first head that kept a chunk owns it: its pair becomes an item
+  {
+    const int GP = GV <= 1 ? 1 : GV <= 2 ? 2 : GV <= 4 ? 4 : 8;
+    const int base = lane & ~(GP - 1), g = lane & (GP - 1);
+    for (int p0 = warp * 32; p0 < n_sel * GP; p0 += TH) {
+      const int pair = (p0 + lane) / GP;
+      const int c = pair < n_sel ? ids[pair] : -1;
+      int at = -1;
+      if (c >= 0 && c < n_cand && g < GV) {
+        const int32_t* list = ids + g * K;
+        int lo = 0, hi = K - 1;
+        while (lo <= hi) {
+          const int mid = (lo + hi) >> 1, v = list[mid];
+          if (v == c) { at = mid; break; }
+          if (v >= 0 && v < c) lo = mid + 1; else hi = mid - 1;
+        }
+      }
+      const uint32_t kept = __ballot_sync(0xffffffffu, at >= 0) >> base;
+      if (at >= 0) {
+        const bool owner = (kept & ((1u << (pair / K)) - 1u)) == 0u;
+        if (owner) spot[pair * 8 + g] = uint8_t(at);
+      } else if (c >= n_cand && g == 0) {
+        record_error(HILS_ERR_DEVICE_BOUNDS);
+      }
+    }
   }
   __syncthreads();
+  // the items: pairs that own their chunk, in order, then the window's chunks
+  int n_items = 0;
+  for (int p0 = 0; p0 < n_sel + n_win; p0 += TH) {
+    const int pair = p0 + tid;
+    int64_t c = -1;
+    if (pair < n_sel) {
+      if (spot[pair * 8 + pair / K] != 0xFF) c = ids[pair];
+    } else if (pair < n_sel + n_win) {
+      c = own - (pair - n_sel);
+    }
+    int page = -1;
+    if (c >= 0) {
+      page = __ldg(table + b * nc + c);
+      if (page < 0 || page >= n_pages) {
+        record_error(HILS_ERR_DEVICE_BOUNDS);
+        page = -1;
+      }
+    }
+    const uint32_t have = __ballot_sync(0xffffffffu, page >= 0);
+    if (lane == 0) s_count[warp] = __popc(have);
+    __syncthreads();
+    int at = n_items + __popc(have & ((1u << lane) - 1u));
+#pragma unroll
+    for (int w = 0; w < kQdWarps; ++w) {
+      if (w < warp) at += s_count[w];
+      n_items += s_count[w];
+    }
+    if (page >= 0) items[at] = make_int2(page, pair < n_sel ? pair : -1 - (pair - n_sel));
+    __syncthreads();
+  }
 
-  // the next slot of this warp at or after s whose chunk is its to attend
+  // item i as this warp attends it
   struct Work {
-    int slot;          // -1: none left
     uint32_t heads;    // who attends the chunk
     float u[2];        // their fusion scores x log2 e (heads 2 tig, 2 tig + 1; selected chunks)
-    const uint8_t *k, *v;
+    int64_t block;
     int keys;
     bool window;
   };
-  const int n_slots = n_sel + n_win, step = int(CL) * kQdWarps;
-  auto find = [&](int s) {
-    Work w{-1, 0u, {0.f, 0.f}, nullptr, nullptr, kChunk, false};
-    for (; s < n_slots; s += step) {
-      int64_t c;
-      float mine = 0.f;
-      if (s >= n_sel) {
-        c = own - (s - n_sel);
-        w.window = true;
-        w.keys = s == n_sel ? n_own : kChunk;
-        w.heads = (1u << GV) - 1u;
-      } else {
-        const int g = s / K;
-        c = ids[s];
-        if (c < 0 || c >= n_cand) {
-          if (c >= 0 && lane == 0) record_error(HILS_ERR_DEVICE_BOUNDS);
-          continue;
-        }
-        bool has = false;
-        if (lane < GV) {
-          int lo = lane * K, hi = lo + K - 1;     // ascending, -1 padding behind
-          while (lo <= hi) {
-            const int mid = (lo + hi) >> 1, v = ids[mid];
-            if (v == c) { has = true; mine = scs[mid] * kLog2e; break; }
-            if (v >= 0 && v < c) lo = mid + 1; else hi = mid - 1;
-          }
-        }
-        w.heads = __ballot_sync(0xffffffffu, has);
-        if (w.heads & ((1u << g) - 1u)) continue;    // an earlier head's slot takes the chunk
-      }
-      int64_t off = 0;
-      if (lane == 0) off = quant_block_offset<D>(table, n_pages, b, h, c, Hkv, nc);
-      off = __shfl_sync(0xffffffffu, off, 0);
-      if (off < 0) { w.window = false; w.keys = kChunk; continue; }
-      w.u[0] = __shfl_sync(0xffffffffu, mine, 2 * tig);
-      w.u[1] = __shfl_sync(0xffffffffu, mine, 2 * tig + 1);
-      w.k = kpg + off;
-      w.v = vpg + off;
-      w.slot = s;
-      return w;
+  const int step = int(CL) * kQdWarps;
+  auto find = [&](int i) {
+    Work w{0u, {0.f, 0.f}, -1, kChunk, false};
+    if (i >= n_items) return w;
+    const int2 it = items[i];
+    w.block = (int64_t(it.x) * Hkv + h) * P::BLOCK;
+    float mine = 0.f;
+    if (it.y < 0) {
+      w.window = true;
+      w.keys = it.y == -1 ? n_own : kChunk;
+      w.heads = (1u << GV) - 1u;
+    } else {
+      const int at = spot[it.y * 8 + (lane & 7)];
+      w.heads = __ballot_sync(0xffffffffu, at != 0xFF) & 0xFFu;
+      if (at != 0xFF) mine = scs[(lane & 7) * K + at];
     }
+    w.u[0] = __shfl_sync(0xffffffffu, mine, 2 * tig);
+    w.u[1] = __shfl_sync(0xffffffffu, mine, 2 * tig + 1);
     return w;
   };
   auto copy = [&](const uint8_t* src, uint32_t dst) {
@@ -422,13 +484,15 @@ quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, co
 #pragma unroll
   for (int i = 0; i < NG * 8; ++i) acc[i / 8][i / 4 % 2][i % 4] = 0.f;
 
-  Work cur = find(int(rank) + warp * int(CL));
-  if (cur.slot >= 0) copy(cur.k, stage_a);
+  int item = int(rank) + warp * int(CL);
+  Work cur = find(item);
+  if (cur.block >= 0) copy(kpg + cur.block, stage_a);
   commit();
-  if (cur.slot >= 0) copy(cur.v, stage_a + A::BLOCK);
+  if (cur.block >= 0) copy(vpg + cur.block, stage_a + A::BLOCK);
   commit();
-  while (cur.slot >= 0) {
-    const Work nxt = find(cur.slot + step);
+  while (cur.block >= 0) {
+    item += step;
+    const Work nxt = find(item);
     wait_all_but_one();
     __syncwarp();
     // ---- logits: tile t, rows are keys 16 t + gid and + 8, columns heads 2 tig, 2 tig + 1
@@ -437,9 +501,11 @@ quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, co
     for (int t = 0; t < 4; ++t) {
       uint32_t cw[2][NG];      // the lane's two units of each group, one register each, for the two rows
       float ps[2][NG], pm[2][NG];
+      uint32_t la[2];          // NS == 1: least values of groups 2 tig, 2 tig + 1
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const int key = 16 * t + 8 * r + gid;
+        const uint8_t* par = stage + P::param_off(key);
         if constexpr (NG == 4) {
           const uint4 u = *reinterpret_cast<const uint4*>(stage + P::code_off(key) + 16 * tig);
           cw[r][0] = __byte_perm(u.x, u.z, 0x5410);
@@ -451,37 +517,50 @@ quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, co
           cw[r][0] = __byte_perm(u.x, u.y, 0x5410);
           cw[r][1] = __byte_perm(u.x, u.y, 0x7632);
         }
-        const __half2* par = reinterpret_cast<const __half2*>(stage + P::param_off(key));
+        if constexpr (NS == 1) {
+          const uint2 m = *reinterpret_cast<const uint2*>(par + 8 * (tig % (NG / 2)));
+          la[r] = tig < NG / 2 ? __byte_perm(m.x, m.y, 0x7632) : 0u;
+        }
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-          const float2 sm = __half22float2(par[g]);
+          const float2 sm = __half22float2(reinterpret_cast<const __half2*>(par)[g]);
           ps[r][g] = sm.x;
-          pm[r][g] = fmaf(-OFF, sm.x, sm.y);
+          pm[r][g] = sm.y;
         }
       }
       z[t][0] = z[t][1] = z[t][2] = z[t][3] = 0.f;
+      // sum_g m_g sum_{i in g} q_i: fp32 models below, else one instruction,
+      // the sums of q split into two fp16 (22 bits)
+      if constexpr (NS == 1) mma16816_f16(z[t], la[0], la[1], la[0], la[1], qs2[0], qs2[1]);
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         uint32_t a[2][4];
         codes_bf16<NS == 3>(cw[0][g], a[0]);
         codes_bf16<NS == 3>(cw[1][g], a[1]);
-        float c[4] = {0.f, 0.f, 0.f, 0.f};
+        float c[4] = {qoff[g][0], qoff[g][1], qoff[g][0], qoff[g][1]};
 #pragma unroll
         for (int n = NS - 1; n >= 0; --n) {
           mma16816_bf16(c, a[0][0], a[1][0], a[0][1], a[1][1], qb[n][g][0], qb[n][g][1]);
           mma16816_bf16(c, a[0][2], a[1][2], a[0][3], a[1][3], qb[n][g][2], qb[n][g][3]);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) z[t][i] = fmaf(ps[i / 2][g], c[i], fmaf(pm[i / 2][g], qsum[g][i % 2], z[t][i]));
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (NS == 1) z[t][i] = g == 0 ? fmaf(z[t][i], 1.f / kSumScale, ps[i / 2][g] * c[i]) : fmaf(ps[i / 2][g], c[i], z[t][i]);
+          else z[t][i] = fmaf(ps[i / 2][g], c[i], fmaf(pm[i / 2][g], qoff[g][i % 2] * (-1.f / OFF), z[t][i]));
+        }
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        z[t][i] *= tau * kLog2e;
-        if (16 * t + 8 * (i / 2) + gid >= cur.keys) z[t][i] = -INFINITY;
-      }
+      for (int i = 0; i < 4; ++i) z[t][i] *= tau * kLog2e;
+    }
+    if (cur.keys < kChunk) {       // the own chunk: keys behind the query
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (16 * t + 8 * (i / 2) + gid >= cur.keys) z[t][i] = -INFINITY;
     }
     __syncwarp();
-    if (nxt.slot >= 0) copy(nxt.k, stage_a);
+    if (nxt.block >= 0) copy(kpg + nxt.block, stage_a);
     commit();
     // ---- the chunk's softmax and its place in the fusion
     float coef[2], alpha[2];
@@ -494,8 +573,8 @@ quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, co
       for (int x = 4; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        z[t][e] = exp2f(z[t][e] - m);
-        z[t][2 + e] = exp2f(z[t][2 + e] - m);
+        z[t][e] = pow2<NS == 1>(z[t][e] - m);
+        z[t][2 + e] = pow2<NS == 1>(z[t][2 + e] - m);
         l += z[t][e] + z[t][2 + e];
       }
 #pragma unroll
@@ -509,12 +588,14 @@ quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, co
       coef[e] = kept ? beta / l : 0.f;
       M[e] = mn;
     }
+    if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
 #pragma unroll
-    for (int g = 0; g < NG; ++g)
+      for (int g = 0; g < NG; ++g)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[g][i / 4][i % 4] *= alpha[i & 1];
-    least[0] *= alpha[0];
-    least[1] *= alpha[1];
+        for (int i = 0; i < 8; ++i) acc[g][i / 4][i % 4] *= alpha[i & 1];
+      least[0] *= alpha[0];
+      least[1] *= alpha[1];
+    }
     wait_all_but_one();
     __syncwarp();
     // ---- output
@@ -539,39 +620,37 @@ quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, co
         }
       }
       uint32_t vc[2][2][NG / 2], vp[2][2][NG];    // codes and parameters of key 16 t + 8 r + 2 tig + j
+      uint32_t vl[2][2];                          // parameters of group gid
 #pragma unroll
       for (int r = 0; r < 2; ++r)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int key = 16 * t + 8 * r + 2 * tig + j;
-          const bool in = key < cur.keys;     // parameters behind the sequence may be anything
           if constexpr (NG == 4) {
             const uint2 u = *reinterpret_cast<const uint2*>(vst + P::code_off(key) + 8 * gid);
             vc[r][j][0] = u.x;
             vc[r][j][1] = u.y;
             const uint4 p = *reinterpret_cast<const uint4*>(vst + P::param_off(key));
-            vp[r][j][0] = in ? p.x : 0u;
-            vp[r][j][1] = in ? p.y : 0u;
-            vp[r][j][2] = in ? p.z : 0u;
-            vp[r][j][3] = in ? p.w : 0u;
+            vp[r][j][0] = p.x;
+            vp[r][j][1] = p.y;
+            vp[r][j][2] = p.z;
+            vp[r][j][3] = p.w;
           } else {
             vc[r][j][0] = *reinterpret_cast<const uint32_t*>(vst + P::code_off(key) + 4 * gid);
             const uint2 p = *reinterpret_cast<const uint2*>(vst + P::param_off(key));
-            vp[r][j][0] = in ? p.x : 0u;
-            vp[r][j][1] = in ? p.y : 0u;
+            vp[r][j][0] = p.x;
+            vp[r][j][1] = p.y;
+          }
+          if constexpr (NS == 1) vl[r][j] = gid < NG ? *reinterpret_cast<const uint32_t*>(vst + P::param_off(key) + 4 * gid) : 0u;
+          if (cur.keys < kChunk && key >= cur.keys) {     // behind the sequence they may be anything
+#pragma unroll
+            for (int g = 0; g < NG; ++g) vp[r][j][g] = 0u;
+            vl[r][j] = 0u;
           }
         }
-      if constexpr (NS == 1) {
-        // least values of group gid as the rows of one product with the weights
-        uint32_t la[2] = {0u, 0u};
-#pragma unroll
-        for (int g = 0; g < NG; ++g)
-          if (gid == g) {
-            la[0] = __byte_perm(vp[0][0][g], vp[0][1][g], 0x7632);
-            la[1] = __byte_perm(vp[1][0][g], vp[1][1][g], 0x7632);
-          }
-        mma16816_f16(lm, la[0], 0u, la[1], 0u, wb[0], wb[1]);
-      }
+      // least values of group gid as the rows of one product with the weights
+      if constexpr (NS == 1)
+        mma16816_f16(lm, __byte_perm(vl[0][0], vl[0][1], 0x7632), 0u, __byte_perm(vl[1][0], vl[1][1], 0x7632), 0u, wb[0], wb[1]);
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         uint32_t x[2];       // units of the two keys of each half side by side
@@ -630,7 +709,7 @@ quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, co
     for (int e = 0; e < 2; ++e)
       if ((cur.heads >> (2 * tig + e)) & 1u) least[e] += lm[e];
     __syncwarp();
-    if (nxt.slot >= 0) copy(nxt.v, stage_a + A::BLOCK);
+    if (nxt.block >= 0) copy(vpg + nxt.block, stage_a + A::BLOCK);
     commit();
     cur = nxt;
   }

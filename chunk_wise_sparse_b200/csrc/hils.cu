@@ -1015,12 +1015,12 @@ int launch_decode_quant(const hils_dims* d, const void* q, const void* q_score, 
   if (e != cudaSuccess) return HILS_ERR_CUDA;
   constexpr auto k3 = quant_attend_kernel<T, D>;
   if (set_smem_max<k3>() != cudaSuccess) return HILS_ERR_CUDA;
-  // CTAs per cluster: enough for every warp to have a chunk, no more than
-  // fill the GPU twice over
+  // CTAs per cluster: as many as run at once (two per SM), unless the warps of
+  // fewer have a chunk each already
   const int n_oct = (G + 7) / 8, heads = G < 8 ? G : 8;
   const int64_t groups = int64_t(bh) * n_oct, slots = int64_t(heads) * K + wm1 + 1;
   unsigned cl = 1;
-  while (cl < 8 && int64_t(cl) * kQdWarps < slots && groups * cl < 2 * sm_count()) cl *= 2;
+  while (cl < 8 && int64_t(cl) * kQdWarps < slots && groups * cl * 2 <= 2 * sm_count()) cl *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(cl, unsigned(groups));
   cfg.blockDim = dim3(kQdWarps * 32);
