@@ -8,7 +8,9 @@ exception is raised.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import struct
 
 import torch
 
@@ -278,37 +280,76 @@ def hils_attn_backward(dims, q, q_score, k, v, lq, kprime, ids, scores, lse_own,
                                     int(nbytes), _stream(stream)))
 
 
-def _rows(t):
+# The serving calls below run once per layer and token: their arguments are marshalled with one device query per call
+# and packed structs.
+
+_PACK_TOKENS, _PACK_ROWS, _PACK_ROTARY = struct.Struct("@qPP"), struct.Struct("@Pqq"), struct.Struct("@Pqii")
+
+
+def _device(t):
+    """The index of the current device, on which t has to be."""
+    dev = t.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        _on_current_device(t)
+    return dev
+
+
+def _dense(t, dev):
+    """Address of a dense tensor on device dev (None is passed on, a raw address as it is)."""
+    if t is None or isinstance(t, int):
+        return t
+    if t.get_device() != dev or not t.is_contiguous():
+        return _ptr(t)
+    return t.data_ptr()
+
+
+def _rows(t, dev):
     """hils_rows of a tensor [T, heads, d] whose last dimension is dense (None is passed on)."""
     if t is None:
         return None
-    _on_current_device(t)
-    if t.dim() != 3 or t.stride(2) != 1:
+    if t.get_device() != dev:
+        _on_current_device(t)
+    st = t.stride()
+    if len(st) != 3 or st[2] != 1:
         raise ValueError(f"expected rows [T, heads, d] with a dense last dimension, got shape {tuple(t.shape)} with "
-                         f"strides {t.stride()}")
-    return ctypes.byref(hils_rows(t.data_ptr(), t.stride(0), t.stride(1)))
+                         f"strides {st}")
+    return _PACK_ROWS.pack(t.data_ptr(), st[0], st[1])
 
 
-def _tokens(seqlens, n_tokens, cu_tokens):
-    cu = None if cu_tokens is None else _ptr(cu_tokens)
-    return ctypes.byref(hils_tokens(int(n_tokens), cu, _ptr(seqlens)))
+def _tokens(seqlens, n_tokens, cu_tokens, dev):
+    return _PACK_TOKENS.pack(n_tokens, _dense(cu_tokens, dev) or 0, _dense(seqlens, dev) or 0)
+
+
+def _rotary(r, dev):
+    if r is None:
+        return None
+    n_pos, rot = r.table.shape
+    return _PACK_ROTARY.pack(_dense(r.table, dev), n_pos, rot, r.interleaved)
+
+
+def _on_stream(stream, dev):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 def hils_kv_append_paged(dims, seqlens, n_tokens, cu_tokens, rotary, q, q_out, k, v, k_pages, v_pages, page_table,
                          n_pages, stream=None):
     """rotary: a Rotary or None; q, q_out, k, v: rows [T, heads, d] with any token and head stride."""
+    dev = _device(k_pages)
     _check("hils_kv_append_paged",
-           lib().hils_kv_append_paged(ctypes.byref(dims), _tokens(seqlens, n_tokens, cu_tokens), _rotary(rotary),
-                                      _rows(q), _rows(q_out), _rows(k), _rows(v), _ptr(k_pages), _ptr(v_pages),
-                                      _ptr(page_table), int(n_pages), _stream(stream)))
+           lib().hils_kv_append_paged(ctypes.byref(dims), _tokens(seqlens, n_tokens, cu_tokens, dev),
+                                      _rotary(rotary, dev), _rows(q, dev), _rows(q_out, dev), _rows(k, dev),
+                                      _rows(v, dev), _dense(k_pages, dev), _dense(v_pages, dev),
+                                      _dense(page_table, dev), n_pages, _on_stream(stream, dev)))
 
 
 def hils_kv_append_quant(dims, seqlens, n_tokens, cu_tokens, rotary, q, q_out, k, v, k_pages, v_pages, page_table,
                          n_pages, stream=None):
+    dev = _device(k_pages)
     _check("hils_kv_append_quant",
-           lib().hils_kv_append_quant(ctypes.byref(dims), _tokens(seqlens, n_tokens, cu_tokens), _rotary(rotary),
-                                      _rows(q), _rows(q_out), _rows(k), _rows(v), _ptr(k_pages), _ptr(v_pages),
-                                      _ptr(page_table), int(n_pages), _stream(stream)))
+           lib().hils_kv_append_quant(ctypes.byref(dims), _tokens(seqlens, n_tokens, cu_tokens, dev),
+                                      _rotary(rotary, dev), _rows(q, dev), _rows(q_out, dev), _rows(k, dev),
+                                      _rows(v, dev), _dense(k_pages, dev), _dense(v_pages, dev),
+                                      _dense(page_table, dev), n_pages, _on_stream(stream, dev)))
 
 
 def hils_quant_page_bytes(dims) -> int:
@@ -316,26 +357,31 @@ def hils_quant_page_bytes(dims) -> int:
 
 
 def hils_kv_read_quant(dims, seqlens, n_tokens, cu_tokens, k_pages, v_pages, page_table, n_pages, k, v, stream=None):
+    dev = _device(page_table)
     _check("hils_kv_read_quant",
-           lib().hils_kv_read_quant(ctypes.byref(dims), _tokens(seqlens, n_tokens, cu_tokens), _ptr(k_pages),
-                                    _ptr(v_pages), _ptr(page_table), int(n_pages), _rows(k), _rows(v),
-                                    _stream(stream)))
+           lib().hils_kv_read_quant(ctypes.byref(dims), _tokens(seqlens, n_tokens, cu_tokens, dev),
+                                    _dense(k_pages, dev), _dense(v_pages, dev), _dense(page_table, dev), n_pages,
+                                    _rows(k, dev), _rows(v, dev), _on_stream(stream, dev)))
 
 
 def hils_landmark_summary_append(dims, seqlens, n_tokens, cu_tokens, k_pages, page_table, n_pages, lq, kprime, bprime,
                                  kprime_mma=None, stream=None):
+    dev = _device(k_pages)
     _check("hils_landmark_summary_append",
-           lib().hils_landmark_summary_append(ctypes.byref(dims), _tokens(seqlens, n_tokens, cu_tokens), _ptr(k_pages),
-                                              _ptr(page_table), int(n_pages), _ptr(lq), _ptr(kprime), _ptr(bprime),
-                                              _ptr(kprime_mma), _stream(stream)))
+           lib().hils_landmark_summary_append(ctypes.byref(dims), _tokens(seqlens, n_tokens, cu_tokens, dev),
+                                              _dense(k_pages, dev), _dense(page_table, dev), n_pages, _dense(lq, dev),
+                                              _dense(kprime, dev), _dense(bprime, dev), _dense(kprime_mma, dev),
+                                              _on_stream(stream, dev)))
 
 
 def hils_landmark_summary_quant(dims, seqlens, n_tokens, cu_tokens, k_pages, page_table, n_pages, lq, kprime, bprime,
                                 kprime_mma=None, stream=None):
+    dev = _device(k_pages)
     _check("hils_landmark_summary_quant",
-           lib().hils_landmark_summary_quant(ctypes.byref(dims), _tokens(seqlens, n_tokens, cu_tokens), _ptr(k_pages),
-                                             _ptr(page_table), int(n_pages), _ptr(lq), _ptr(kprime), _ptr(bprime),
-                                             _ptr(kprime_mma), _stream(stream)))
+           lib().hils_landmark_summary_quant(ctypes.byref(dims), _tokens(seqlens, n_tokens, cu_tokens, dev),
+                                             _dense(k_pages, dev), _dense(page_table, dev), n_pages, _dense(lq, dev),
+                                             _dense(kprime, dev), _dense(bprime, dev), _dense(kprime_mma, dev),
+                                             _on_stream(stream, dev)))
 
 
 def hils_decode_quant_workspace_bytes(dims) -> int:
@@ -344,12 +390,14 @@ def hils_decode_quant_workspace_bytes(dims) -> int:
 
 def hils_attn_decode_quant(dims, q, q_score, k_pages, v_pages, page_table, n_pages, kprime, bprime, kprime_mma,
                            seqlens, o, ids_out, scores_out, workspace, workspace_bytes=None, stream=None):
+    dev = _device(q)
     nbytes = workspace.numel() * workspace.element_size() if workspace_bytes is None else workspace_bytes
     _check("hils_attn_decode_quant",
-           lib().hils_attn_decode_quant(ctypes.byref(dims), _ptr(q), _ptr(q_score), _ptr(k_pages), _ptr(v_pages),
-                                        _ptr(page_table), int(n_pages), _ptr(kprime), _ptr(bprime), _ptr(kprime_mma),
-                                        _ptr(seqlens), _ptr(o), _ptr(ids_out), _ptr(scores_out), _ptr(workspace),
-                                        int(nbytes), _stream(stream)))
+           lib().hils_attn_decode_quant(ctypes.byref(dims), _dense(q, dev), _dense(q_score, dev), _dense(k_pages, dev),
+                                        _dense(v_pages, dev), _dense(page_table, dev), n_pages, _dense(kprime, dev),
+                                        _dense(bprime, dev), _dense(kprime_mma, dev), _dense(seqlens, dev),
+                                        _dense(o, dev), _dense(ids_out, dev), _dense(scores_out, dev),
+                                        _dense(workspace, dev), nbytes, _on_stream(stream, dev)))
 
 
 def hils_get_status(stream=None) -> int:
@@ -518,8 +566,9 @@ class Rotary:
     __slots__ = ("table", "interleaved")
 
     def __init__(self, table, interleaved=False):
-        _need(table, "rotary table", torch.float32, (None, None))
-        self.table, self.interleaved = table, bool(interleaved)
+        if table.dim() != 2 or table.dtype is not torch.float32:
+            raise ValueError(f"rotary table: expected fp32 [n_pos, rot_dim], got {table.dtype} {tuple(table.shape)}")
+        self.table, self.interleaved = table, int(bool(interleaved))
 
 
 def rotary_table(n_pos, rot_dim, base=10000.0, device="cuda"):
@@ -530,15 +579,10 @@ def rotary_table(n_pos, rot_dim, base=10000.0, device="cuda"):
     return torch.cat([angle.cos(), angle.sin()], 1).float()
 
 
-def _rotary(r):
-    if r is None:
-        return None
-    n_pos, rot = r.table.shape
-    return ctypes.byref(hils_rotary(_ptr(r.table), n_pos, rot, int(r.interleaved)))
-
-
 def _need(t, name, dtype, shape):
     """Refuse a tensor of another type or shape (None: any extent)."""
+    if t.dtype is dtype and t.shape == shape:
+        return
     if t.dtype != dtype or t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
         raise ValueError(f"{name}: expected {dtype} {tuple('any' if n is None else n for n in shape)}, got {t.dtype} "
                          f"{tuple(t.shape)}")
@@ -546,45 +590,47 @@ def _need(t, name, dtype, shape):
 
 def _page_kind(k_pages, v_pages, dtype):
     """(4-bit?, n_pages, Hkv, d) of a pair of pools (v_pages None: keys alone)."""
-    if v_pages is not None and (v_pages.shape != k_pages.shape or v_pages.dtype != k_pages.dtype):
-        raise ValueError(f"key pages {k_pages.dtype} {tuple(k_pages.shape)} and value pages {v_pages.dtype} "
-                         f"{tuple(v_pages.shape)} differ")
-    if k_pages.dtype == torch.uint8:
-        if k_pages.dim() != 3 or k_pages.shape[2] not in (40 * CHUNK, 80 * CHUNK):
-            raise ValueError(f"4-bit pages are [n_pages, Hkv, 64 * (d/2 + d/8)], got {tuple(k_pages.shape)}")
-        return True, k_pages.shape[0], k_pages.shape[1], k_pages.shape[2] // 40
-    if k_pages.dim() != 4 or k_pages.shape[2] != CHUNK or k_pages.dtype != dtype:
-        raise ValueError(f"expected {dtype} pages [n_pages, Hkv, 64, d] or 4-bit ones, got {k_pages.dtype} "
-                         f"{tuple(k_pages.shape)}")
-    return False, k_pages.shape[0], k_pages.shape[1], k_pages.shape[3]
+    shape, kind = k_pages.shape, k_pages.dtype
+    if v_pages is not None and (v_pages.shape != shape or v_pages.dtype is not kind):
+        raise ValueError(f"key pages {kind} {tuple(shape)} and value pages {v_pages.dtype} {tuple(v_pages.shape)} differ")
+    if kind is torch.uint8:
+        if len(shape) != 3 or shape[2] not in (40 * CHUNK, 80 * CHUNK):
+            raise ValueError(f"4-bit pages are [n_pages, Hkv, 64 * (d/2 + d/8)], got {tuple(shape)}")
+        return True, shape[0], shape[1], shape[2] // 40
+    if len(shape) != 4 or shape[2] != CHUNK or kind is not dtype:
+        raise ValueError(f"expected {dtype} pages [n_pages, Hkv, 64, d] or 4-bit ones, got {kind} {tuple(shape)}")
+    return False, shape[0], shape[1], shape[3]
 
 
 def _batch(page_table, seqlens, cu_tokens):
     """(B, nc) of a ragged batch."""
-    _need(page_table, "page_table", torch.int32, (None, None))
-    B, nc = page_table.shape
+    if page_table.dim() != 2:
+        raise ValueError(f"page_table: expected [B, nc], got {tuple(page_table.shape)}")
+    B, nc = shape = page_table.shape
+    _need(page_table, "page_table", torch.int32, shape)
     _need(seqlens, "seqlens", torch.int32, (B,))
     if cu_tokens is not None:
         _need(cu_tokens, "cu_tokens", torch.int32, (B + 1,))
     return B, nc
 
 
-class _on:
-    """Allocate on the stream that the kernels will run on, so that the caching allocator gives the memory to no other
-    stream's work before they end."""
+@functools.lru_cache(maxsize=1024)
+def _dims_of(B, Hq, Hkv, d, nc, topk, dtype, window):
+    return make_dims(B, Hq, Hkv, d, nc * CHUNK, topk, dtype, window=window)
 
-    def __init__(self, stream):
-        if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream)
-        self.ctx = None if stream is None else torch.cuda.stream(stream)
 
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
+@functools.lru_cache(maxsize=1024)
+def _decode_quant_bytes(B, Hq, Hkv, d, nc, topk, dtype, window):
+    return hils_decode_quant_workspace_bytes(_dims_of(B, Hq, Hkv, d, nc, topk, dtype, window))
 
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+
+def _new(like, shape, dtype, stream):
+    """A new tensor on the stream that the kernels will run on, so that the caching allocator gives its memory to no
+    other stream's work before they end."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream):
+        return like.new_empty(shape, dtype=dtype)
 
 
 def quant_pages(n_pages, heads_kv, head_dim, device="cuda"):
@@ -601,25 +647,24 @@ def kv_append(k_pages, v_pages, page_table, k, v, seqlens, cu_tokens=None, rotar
     """Append the packed new keys and values k, v [T,Hkv,d] to a chunk-paged cache (bf16 / fp32 or 4-bit pages),
     rotating keys, and queries q [T,Hq,d], by their positions.  k, v, q may be views with any token and head stride.
     Returns the rotated queries (q_out, or a new [T,Hq,d]; None without q)."""
-    quant, n_pages, Hkv, d = _page_kind(k_pages, v_pages, k.dtype)
+    dtype = k.dtype
+    quant, n_pages, Hkv, d = _page_kind(k_pages, v_pages, dtype)
     B, nc = _batch(page_table, seqlens, cu_tokens)
-    T = k.shape[0]
-    _need(k, "k", k.dtype, (T, Hkv, d))
-    _need(v, "v", k.dtype, (T, Hkv, d))
-    Hq = Hkv
+    T, Hq = k.shape[0], Hkv
+    _need(k, "k", dtype, (T, Hkv, d))
+    _need(v, "v", dtype, (T, Hkv, d))
     if q is not None:
         Hq = q.shape[1]
-        _need(q, "q", k.dtype, (T, Hq, d))
+        _need(q, "q", dtype, (T, Hq, d))
         if q_out is None:
-            with _on(stream):
-                q_out = torch.empty((T, Hq, d), dtype=k.dtype, device=k.device)
+            q_out = _new(k, (T, Hq, d), dtype, stream)
         else:
-            _need(q_out, "q_out", k.dtype, (T, Hq, d))
+            _need(q_out, "q_out", dtype, (T, Hq, d))
     elif q_out is not None:
         raise ValueError("q_out without q")
-    dims = make_dims(B, Hq, Hkv, d, nc * CHUNK, 1, k.dtype)
     call = hils_kv_append_quant if quant else hils_kv_append_paged
-    call(dims, seqlens, T, cu_tokens, rotary, q, q_out, k, v, k_pages, v_pages, page_table, n_pages, stream)
+    call(_dims_of(B, Hq, Hkv, d, nc, 1, dtype, 0), seqlens, T, cu_tokens, rotary, q, q_out, k, v, k_pages, v_pages,
+         page_table, n_pages, stream)
     return q_out
 
 
@@ -631,17 +676,18 @@ def kv_read(k_pages, v_pages, page_table, seqlens, n_tokens, dtype, cu_tokens=No
     if not quant:
         raise ValueError("kv_read reads 4-bit pages")
     B, nc = _batch(page_table, seqlens, cu_tokens)
-    out = []
-    for name, t in (("k_out", k_out), ("v_out", v_out)):
-        if t is None:
-            with _on(stream):
-                t = torch.empty((n_tokens, Hkv, d), dtype=dtype, device=k_pages.device)
-        else:
-            _need(t, name, dtype, (n_tokens, Hkv, d))
-        out.append(t)
-    dims = make_dims(B, Hkv, Hkv, d, nc * CHUNK, 1, dtype)
-    hils_kv_read_quant(dims, seqlens, n_tokens, cu_tokens, k_pages, v_pages, page_table, n_pages, *out, stream)
-    return tuple(out)
+    shape = (n_tokens, Hkv, d)
+    if k_out is None:
+        k_out = _new(k_pages, shape, dtype, stream)
+    else:
+        _need(k_out, "k_out", dtype, shape)
+    if v_out is None:
+        v_out = _new(k_pages, shape, dtype, stream)
+    else:
+        _need(v_out, "v_out", dtype, shape)
+    hils_kv_read_quant(_dims_of(B, Hkv, Hkv, d, nc, 1, dtype, 0), seqlens, n_tokens, cu_tokens, k_pages, v_pages,
+                       page_table, n_pages, k_out, v_out, stream)
+    return k_out, v_out
 
 
 def _need_summary(summ, B, Hkv, nc, d, dtype):
@@ -660,9 +706,8 @@ def landmark_summary_append(k_pages, page_table, lq, seqlens, n_tokens, summ: Su
     B, nc = _batch(page_table, seqlens, cu_tokens)
     _need(lq, "lq", lq.dtype, (B, Hkv, nc, d))
     _need_summary(summ, B, Hkv, nc, d, lq.dtype)
-    dims = make_dims(B, Hkv, Hkv, d, nc * CHUNK, 1, lq.dtype)
     call = hils_landmark_summary_quant if quant else hils_landmark_summary_append
-    call(dims, seqlens, n_tokens, cu_tokens, k_pages, page_table, n_pages, lq, summ.kprime, summ.bprime,
+    call(_dims_of(B, Hkv, Hkv, d, nc, 1, lq.dtype, 0), seqlens, n_tokens, cu_tokens, k_pages, page_table, n_pages, lq, summ.kprime, summ.bprime,
          summ.kprime_mma, stream)
     return summ
 
@@ -671,25 +716,25 @@ def decode_step_quant(q, k_pages, v_pages, page_table, summ: Summary, seqlens, t
                       stream=None, window=0, out=None):
     """One decode step for q [B,Hq,d] against a 4-bit chunk-paged cache; q_score: a separate scoring query (Q-Cal).
     Returns (o, ids, scores)."""
-    B, Hq, d = q.shape
-    quant, n_pages, Hkv, d_pages = _page_kind(k_pages, v_pages, q.dtype)
+    dtype = q.dtype
+    quant, n_pages, Hkv, d = _page_kind(k_pages, v_pages, dtype)
     if not quant:
         raise ValueError("decode_step_quant reads 4-bit pages")
-    _, nc = _batch(page_table, seqlens, None)
-    _need(q, "q", q.dtype, (page_table.shape[0], None, d_pages))
+    B, nc = _batch(page_table, seqlens, None)
+    Hq = q.shape[1]
+    _need(q, "q", dtype, (B, Hq, d))
     if q_score is not None:
-        _need(q_score, "q_score", q.dtype, (B, Hq, d))
-    _need_summary(summ, B, Hkv, nc, d, q.dtype)
-    dims = make_dims(B, Hq, Hkv, d, nc * CHUNK, topk, q.dtype, window=window)
-    with _on(stream):
-        if workspace is None:
-            workspace = torch.empty((hils_decode_quant_workspace_bytes(dims),), dtype=torch.uint8, device=q.device)
-        if out is None:
-            out = torch.empty_like(q)
-        else:
-            _need(out, "out", q.dtype, (B, Hq, d))
-        ids = torch.empty((B, Hq, topk), dtype=torch.int32, device=q.device)
-        scores = torch.empty((B, Hq, topk), dtype=torch.float32, device=q.device)
-    hils_attn_decode_quant(dims, q, q_score, k_pages, v_pages, page_table, n_pages, summ.kprime, summ.bprime,
-                           summ.kprime_mma, seqlens, out, ids, scores, workspace, stream=stream)
+        _need(q_score, "q_score", dtype, (B, Hq, d))
+    _need_summary(summ, B, Hkv, nc, d, dtype)
+    key = (B, Hq, Hkv, d, nc, topk, dtype, window)
+    if workspace is None:
+        workspace = _new(q, (_decode_quant_bytes(*key),), torch.uint8, stream)
+    if out is None:
+        out = _new(q, (B, Hq, d), dtype, stream)
+    else:
+        _need(out, "out", dtype, (B, Hq, d))
+    ids = _new(q, (B, Hq, topk), torch.int32, stream)
+    scores = _new(q, (B, Hq, topk), torch.float32, stream)
+    hils_attn_decode_quant(_dims_of(*key), q, q_score, k_pages, v_pages, page_table, n_pages, summ.kprime, summ.bprime,
+                           summ.kprime_mma, seqlens, out, ids, scores, workspace, workspace.nbytes, stream)
     return out, ids, scores
