@@ -50,6 +50,28 @@ __device__ __forceinline__ Place find_place(const TokenBatch& tb, int64_t t) {
   return place_in(tb, t, lo, __ldg(tb.cu + lo), __ldg(tb.cu + lo + 1));
 }
 
+// The place of token t (the same for the whole warp): the last b with
+// cu[b] <= t by a 32-way search, one load per lane and round, so that a batch
+// of up to 32 sequences costs one load latency and one of up to 1024 two.
+__device__ __forceinline__ Place find_place_warp(const TokenBatch& tb, int64_t t, int lane) {
+  if (tb.cu == nullptr) {
+    const int64_t b = t / tb.per;
+    return place_in(tb, t, b, b * tb.per, (b + 1) * tb.per);
+  }
+  const int end = __ldg(tb.cu + tb.batch);
+  int lo = 0, len = tb.batch;
+  while (len > 1) {
+    const int step = (len + 31) / 32, at = lane * step;
+    const bool low = at < len && __ldg(tb.cu + lo + at) <= t;
+    const int n = __popc(__ballot_sync(0xffffffffu, low));
+    const int skip = n > 0 ? (n - 1) * step : 0;
+    lo += skip;
+    len = len - skip < step ? len - skip : step;
+  }
+  if (t >= end) return Place{-1, 0};     // padding
+  return place_in(tb, t, lo, __ldg(tb.cu + lo), __ldg(tb.cu + lo + 1));
+}
+
 // One block (or warp) of a launch looks at the whole of cu_tokens: it has to
 // ascend from 0 to at most n_tokens.
 __device__ __forceinline__ void check_batch(const TokenBatch& tb, int thread, int threads) {
@@ -75,27 +97,52 @@ struct AppendParams {
   int64_t n_pos;
   int rot, interleaved;
   int Hq, Hkv;
+  int shares, per_share;        // warps per token, and steps of KPI rows of each
 };
 
-// One CTA per token.  A row (one head of q, k or v) is held by D / E lanes, a
-// 16-byte vector each; the angles of the lane's dims are loaded once and used
-// for all of its rows.  y = x c + x' s' with x' the other element of the
-// pair (another lane's in the half-split style, fetched by a shuffle).
+// A 16-byte piece as E fp32 values.
+template <typename T>
+__device__ __forceinline__ void widen(uint4 w, float (&x)[Vec16<T>::E]) {
+  if constexpr (Vec16<T>::E == 8) {
+    Vec16<T>::unpack(w, x);
+  } else {
+    x[0] = __uint_as_float(w.x);
+    x[1] = __uint_as_float(w.y);
+    x[2] = __uint_as_float(w.z);
+    x[3] = __uint_as_float(w.w);
+  }
+}
+
+// One warp per (token, share of its rows).  A row (one head of q, k or v) is
+// held by LPR = d / E lanes, a 16-byte piece each, KPI = 32 / LPR rows at a
+// time; the token's place and the angles of the lane's dims are found once and
+// used for all rows of the warp.  y = x c + x' s' with x' the other element of
+// the pair (another lane's in the half-split style, fetched by a shuffle).
+// The kinds of row are padded to KPI rows each, so that the warp always works
+// on one kind.  HBM-bound for a prompt; kAppendUnroll pieces per lane are in
+// flight at once.  `share` rows per warp: see launch_append.
+constexpr int kAppendUnroll = 4;
+
 template <typename T, int D, bool Q4>
-__global__ void __launch_bounds__(256) kv_append_kernel(AppendParams p) {
-  constexpr int E = Vec16<T>::E, LPR = D / E, RPP = 256 / LPR;
-  const int64_t t = blockIdx.x;
-  if (t == 0) check_batch(p.tb, threadIdx.x, 256);
-  const Place at = find_place(p.tb, t);
+__global__ void __launch_bounds__(128) kv_append_kernel(AppendParams p) {
+  constexpr int E = Vec16<T>::E, LPR = D / E, KPI = 32 / LPR, U = kAppendUnroll;
+  const int lane = threadIdx.x & 31, sub = lane % LPR, grp = lane / LPR;
+  if (blockIdx.x == 0) check_batch(p.tb, threadIdx.x, 128);
+  const int64_t item = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  const int64_t t = item / p.shares;
+  if (t >= p.tb.n_tokens) return;
+  const int nq = p.q.data ? (p.Hq + KPI - 1) / KPI : 0, nk = (p.Hkv + KPI - 1) / KPI;
+  const int it0 = int(item % p.shares) * p.per_share;
+  const int it1 = it0 + p.per_share < nq + 2 * nk ? it0 + p.per_share : nq + 2 * nk;
+  const Place at = find_place_warp(p.tb, t, lane);
   if (at.b < 0) return;
   if (p.rot > 0 && at.pos >= p.n_pos) {
-    if (threadIdx.x == 0) record_error(HILS_ERR_DEVICE_BOUNDS);
+    if (lane == 0) record_error(HILS_ERR_DEVICE_BOUNDS);
     return;
   }
-  const int sub = threadIdx.x % LPR, row0 = threadIdx.x / LPR, lane = threadIdx.x & 31;
   const int64_t page = __ldg(p.table + at.b * p.nc + at.pos / kChunk);
   const bool in_pool = page >= 0 && page < p.n_pages;
-  if (!in_pool && threadIdx.x == 0) record_error(HILS_ERR_DEVICE_BOUNDS);
+  if (!in_pool && lane == 0) record_error(HILS_ERR_DEVICE_BOUNDS);
   const int in_chunk = int(at.pos % kChunk);
   // the angles of this lane's dims, the sign of the second term in `s`
   const int dim0 = sub * E, half = p.rot / 2;
@@ -104,66 +151,77 @@ __global__ void __launch_bounds__(256) kv_append_kernel(AppendParams p) {
   int partner = lane;
   if (turns) {
     const float* tr = p.rotary + at.pos * p.rot;
+    if (p.interleaved) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int i = p.interleaved ? (dim0 + e) / 2 : (dim0 + e) % half;
-      const bool second = p.interleaved ? (e & 1) : dim0 >= half;
-      c[e] = __ldg(tr + i);
-      const float sn = __ldg(tr + half + i);
-      s[e] = second ? sn : -sn;
+      for (int e = 0; e < E; e += 2) {
+        c[e] = c[e + 1] = __ldg(tr + (dim0 + e) / 2);
+        s[e + 1] = __ldg(tr + half + (dim0 + e) / 2);
+        s[e] = -s[e + 1];
+      }
+    } else {
+      const bool second = dim0 >= half;
+      const int i = second ? dim0 - half : dim0;     // half is a multiple of 8, E at most 8
+      partner = second ? lane - half / E : lane + half / E;
+#pragma unroll
+      for (int e = 0; e < E; e += 4) {
+        const float4 cv = __ldg(reinterpret_cast<const float4*>(tr + i + e)), sv = __ldg(reinterpret_cast<const float4*>(tr + half + i + e));
+        c[e] = cv.x; c[e + 1] = cv.y; c[e + 2] = cv.z; c[e + 3] = cv.w;
+        s[e] = second ? sv.x : -sv.x; s[e + 1] = second ? sv.y : -sv.y;
+        s[e + 2] = second ? sv.z : -sv.z; s[e + 3] = second ? sv.w : -sv.w;
+      }
     }
-    if (!p.interleaved) partner = lane + (dim0 < half ? half / E : -(half / E));
   }
-  const int Hq = p.q.data ? p.Hq : 0, total = Hq + 2 * p.Hkv;
-  for (int r0 = 0; r0 < total; r0 += RPP) {
-    const int r = r0 + row0;
-    const bool live = r < total;
-    const int kind = r < Hq ? 0 : r < Hq + p.Hkv ? 1 : 2;    // query, key, value
-    const int h = kind == 0 ? r : r - Hq - (kind - 1) * p.Hkv;
-    const RowsView& src = kind == 0 ? p.q : kind == 1 ? p.k : p.v;
-    uint4 w = make_uint4(0, 0, 0, 0);
-    if (live) w = *reinterpret_cast<const uint4*>(static_cast<const T*>(src.data) + t * src.ts + h * src.hs + dim0);
-    float x[E], y[E];
-    if constexpr (E == 8) {
-      Vec16<T>::unpack(w, x);
-    } else {
-      x[0] = __uint_as_float(w.x); x[1] = __uint_as_float(w.y); x[2] = __uint_as_float(w.z); x[3] = __uint_as_float(w.w);
-    }
-    if (p.rot > 0) {
-      uint4 o;
-      o.x = __shfl_sync(0xffffffffu, w.x, partner);
-      o.y = __shfl_sync(0xffffffffu, w.y, partner);
-      o.z = __shfl_sync(0xffffffffu, w.z, partner);
-      o.w = __shfl_sync(0xffffffffu, w.w, partner);
-      float z[E];
-      if constexpr (E == 8) {
-        Vec16<T>::unpack(o, z);
-      } else {
-        z[0] = __uint_as_float(o.x); z[1] = __uint_as_float(o.y); z[2] = __uint_as_float(o.z); z[3] = __uint_as_float(o.w);
-      }
-      if (turns && kind < 2) {
+  for (int i0 = it0; i0 < it1; i0 += U) {
+    uint4 w[U];
 #pragma unroll
-        for (int e = 0; e < E; ++e) y[e] = fmaf(x[e], c[e], (p.interleaved ? x[e ^ 1] : z[e]) * s[e]);
+    for (int u = 0; u < U; ++u) {
+      const int it = i0 + u;
+      const int kind = it < nq ? 0 : it < nq + nk ? 1 : 2;    // query, key, value
+      const int h = (it - (kind == 0 ? 0 : nq + (kind - 1) * nk)) * KPI + grp;
+      const RowsView& src = kind == 0 ? p.q : kind == 1 ? p.k : p.v;
+      w[u] = make_uint4(0, 0, 0, 0);
+      if (it < it1 && h < (kind == 0 ? p.Hq : p.Hkv))
+        w[u] = *reinterpret_cast<const uint4*>(static_cast<const T*>(src.data) + t * src.ts + h * src.hs + dim0);
+    }
 #pragma unroll
-        for (int e = 0; e < E; ++e) x[e] = y[e];
+    for (int u = 0; u < U; ++u) {
+      const int it = i0 + u;
+      if (it >= it1) break;
+      const int kind = it < nq ? 0 : it < nq + nk ? 1 : 2;
+      const int h = (it - (kind == 0 ? 0 : nq + (kind - 1) * nk)) * KPI + grp;
+      const bool live = h < (kind == 0 ? p.Hq : p.Hkv);
+      float x[E];
+      widen<T>(w[u], x);
+      if (p.rot > 0 && kind < 2) {
+        float z[E];
+        if (p.interleaved) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) z[e] = x[e ^ 1];
+        } else {
+          uint4 o;
+          o.x = __shfl_sync(0xffffffffu, w[u].x, partner);
+          o.y = __shfl_sync(0xffffffffu, w[u].y, partner);
+          o.z = __shfl_sync(0xffffffffu, w[u].z, partner);
+          o.w = __shfl_sync(0xffffffffu, w[u].w, partner);
+          widen<T>(o, z);
+        }
+        if (turns) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) x[e] = fmaf(x[e], c[e], z[e] * s[e]);
+        }
       }
+      if (kind == 0) {
+        if (live) Vec16<T>::store(static_cast<T*>(p.q_out.data) + t * p.q_out.ts + h * p.q_out.hs + dim0, x);
+        continue;
+      }
+      void* pool = kind == 1 ? p.k_pages : p.v_pages;
+      const bool store = live && in_pool;
+      const int64_t row = store ? page * p.Hkv + h : 0;
+      if constexpr (Q4)
+        quant_store_row<D, E>(x, sub, static_cast<uint8_t*>(pool) + row * QuantPage<D>::BLOCK, in_chunk, store);
+      else if (store)
+        Vec16<T>::store(static_cast<T*>(pool) + (row * kChunk + in_chunk) * D + dim0, x);
     }
-    if constexpr (Q4) {
-      // every lane takes part in the shuffles, the rows of queries without storing
-      uint8_t* pool = static_cast<uint8_t*>(kind == 1 ? p.k_pages : p.v_pages);
-      const bool store = live && in_pool && kind > 0;
-      quant_store_row<D, E>(x, sub, pool + (store ? (page * p.Hkv + h) * QuantPage<D>::BLOCK : 0), in_chunk, store);
-      if (kind > 0) continue;
-    }
-    if (!live) continue;
-    T* dst;
-    if (kind == 0) {
-      dst = static_cast<T*>(p.q_out.data) + t * p.q_out.ts + h * p.q_out.hs;
-    } else {
-      if (!in_pool) continue;
-      dst = static_cast<T*>(kind == 1 ? p.k_pages : p.v_pages) + ((page * p.Hkv + h) * kChunk + in_chunk) * D;
-    }
-    Vec16<T>::store(dst + dim0, x);
   }
 }
 
@@ -173,32 +231,83 @@ struct ReadParams {
   const uint8_t *k_pages, *v_pages;
   const int32_t* table;
   int64_t n_pages, nc;
-  int Hkv;
+  int Hkv, shares, per_share;
 };
 
-// One CTA per token, D / E lanes per row.
+// One warp per (eight packed tokens, share of the heads): four lanes per token
+// read d / 8 bytes of codes each, which are eight neighbouring dims of every
+// group, and store those as one piece per group.  HBM-bound: 5 d / 8 bytes in,
+// d elements out per row.
 template <typename T, int D>
-__global__ void __launch_bounds__(256) kv_read_quant_kernel(ReadParams p) {
-  constexpr int E = Vec16<T>::E, LPR = D / E, RPP = 256 / LPR;
-  const int64_t t = blockIdx.x;
-  if (t == 0) check_batch(p.tb, threadIdx.x, 256);
-  const Place at = find_place(p.tb, t);
-  if (at.b < 0) return;
+__global__ void __launch_bounds__(128) kv_read_quant_kernel(ReadParams p) {
+  using P = QuantPage<D>;
+  constexpr int NG = P::G, U = 2;
+  const int lane = threadIdx.x & 31, tok = lane >> 2, part = lane & 3;
+  if (blockIdx.x == 0) check_batch(p.tb, threadIdx.x, 128);
+  const int64_t item = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  const int64_t t = item / p.shares * 8 + tok;
+  if (item / p.shares * 8 >= p.tb.n_tokens) return;
+  const int r0 = int(item % p.shares) * p.per_share;
+  const int r1 = r0 + p.per_share < 2 * p.Hkv ? r0 + p.per_share : 2 * p.Hkv;
+  Place at{-1, 0};
+  if (t < p.tb.n_tokens) at = find_place(p.tb, t);
+  if (at.b < 0) return;      // no shuffles below
   const int64_t page = __ldg(p.table + at.b * p.nc + at.pos / kChunk);
   if (page < 0 || page >= p.n_pages) {
-    if (threadIdx.x == 0) record_error(HILS_ERR_DEVICE_BOUNDS);
+    record_error(HILS_ERR_DEVICE_BOUNDS);
     return;
   }
-  const int sub = threadIdx.x % LPR;
-  for (int r = threadIdx.x / LPR; r < 2 * p.Hkv; r += RPP) {
-    const bool key = r < p.Hkv;
-    const RowsView& dst = key ? p.k : p.v;
-    if (dst.data == nullptr) continue;
-    const int h = key ? r : r - p.Hkv;
-    float x[E];
-    quant_load_row<D, E>((key ? p.k_pages : p.v_pages) + (page * p.Hkv + h) * QuantPage<D>::BLOCK, int(at.pos % kChunk),
-                         sub, x);
-    Vec16<T>::store(static_cast<T*>(dst.data) + t * dst.ts + h * dst.hs + sub * E, x);
+  const int row = int(at.pos % kChunk);
+  for (int i0 = r0; i0 < r1; i0 += U) {
+    uint32_t code[U][NG], par[U][NG];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int r = i0 + u;
+      const bool key = r < p.Hkv;
+      const uint8_t* pool = key ? p.k_pages : p.v_pages;
+      if (r >= r1 || (key ? p.k.data : p.v.data) == nullptr) continue;
+      const uint8_t* block = pool + (page * p.Hkv + (key ? r : r - p.Hkv)) * P::BLOCK;
+      if constexpr (NG == 4) {
+        const uint4 a = __ldg(reinterpret_cast<const uint4*>(block + P::code_off(row) + 16 * part));
+        const uint4 b = __ldg(reinterpret_cast<const uint4*>(block + P::param_off(row)));
+        code[u][0] = a.x; code[u][1] = a.y; code[u][2] = a.z; code[u][3] = a.w;
+        par[u][0] = b.x; par[u][1] = b.y; par[u][2] = b.z; par[u][3] = b.w;
+      } else {
+        const uint2 a = __ldg(reinterpret_cast<const uint2*>(block + P::code_off(row) + 8 * part));
+        const uint2 b = __ldg(reinterpret_cast<const uint2*>(block + P::param_off(row)));
+        code[u][0] = a.x; code[u][1] = a.y;
+        par[u][0] = b.x; par[u][1] = b.y;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int r = i0 + u;
+      const bool key = r < p.Hkv;
+      const RowsView& dst = key ? p.k : p.v;
+      if (r >= r1 || dst.data == nullptr) continue;
+      T* out = static_cast<T*>(dst.data) + t * dst.ts + (key ? r : r - p.Hkv) * dst.hs + 8 * part;
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        // words are units (2 part, g), (2 part, g + 1), .. , then those of 2 part + 1
+        const uint32_t w = __byte_perm(code[u][g / 2], code[u][NG / 2 + g / 2], g & 1 ? 0x7632 : 0x5410);
+        const __half2 sm = *reinterpret_cast<const __half2*>(&par[u][g]);
+        const float s = __low2float(sm), m = __high2float(sm);
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          // bf16 128 + code: exact in fp32 after taking the offset off again
+          const uint32_t v = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+          x[i] = fmaf(s, __uint_as_float(v << 16) - 128.f, m);
+          x[i + 4] = fmaf(s, __uint_as_float(v & 0xFFFF0000u) - 128.f, m);
+        }
+        if constexpr (sizeof(T) == 2) {
+          Vec16<T>::store(out + 32 * g, x);
+        } else {
+          *reinterpret_cast<float4*>(out + 32 * g) = make_float4(x[0], x[1], x[2], x[3]);
+          *reinterpret_cast<float4*>(out + 32 * g + 4) = make_float4(x[4], x[5], x[6], x[7]);
+        }
+      }
+    }
   }
 }
 

@@ -861,9 +861,25 @@ static RowsView rows_view(const hils_rows* r) {
 
 namespace {
 
+// How the `steps` steps of a token are shared out to warps: a share of up to
+// `most` steps where the tokens fill the GPU, fewer where they do not (a
+// decode step of one sequence spreads its rows over as many warps).
+void share_steps(int64_t tokens, int steps, int most, int* shares, int* per_share) {
+  const int64_t warps = int64_t(sm_count()) * 32;
+  int64_t s = (steps + most - 1) / most;
+  if (tokens * s < warps) s = (warps + tokens - 1) / tokens < steps ? (warps + tokens - 1) / tokens : steps;
+  *per_share = int((steps + s - 1) / s);
+  *shares = (steps + *per_share - 1) / *per_share;
+}
+
 template <typename T, int D, bool Q4>
-int launch_append(const AppendParams& p, cudaStream_t st) {
-  kv_append_kernel<T, D, Q4><<<unsigned(p.tb.n_tokens), 256, 0, st>>>(p);
+int launch_append(AppendParams p, cudaStream_t st) {
+  constexpr int KPI = 32 / (D / Vec16<T>::E);
+  const int steps = (p.q.data ? (p.Hq + KPI - 1) / KPI : 0) + 2 * ((p.Hkv + KPI - 1) / KPI);
+  share_steps(p.tb.n_tokens, steps, 4 * kAppendUnroll, &p.shares, &p.per_share);
+  const int64_t blocks = (p.tb.n_tokens * p.shares + 3) / 4;
+  if (blocks >= (int64_t(1) << 31)) return HILS_ERR_UNSUPPORTED;
+  kv_append_kernel<T, D, Q4><<<unsigned(blocks), 128, 0, st>>>(p);
   return launched(1);
 }
 
@@ -1084,13 +1100,17 @@ int hils_kv_read_quant(const hils_dims* d, const hils_tokens* tokens, const void
   p.nc = d->seqlen / kChunk;
   p.Hkv = d->heads_kv;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const unsigned grid = unsigned(T);
+  const int64_t eights = (T + 7) / 8;
+  share_steps(eights, 2 * p.Hkv, 8, &p.shares, &p.per_share);
+  const int64_t blocks = (eights * p.shares + 3) / 4;
+  if (blocks >= (int64_t(1) << 31)) return HILS_ERR_UNSUPPORTED;
+  const unsigned grid = unsigned(blocks);
   if (d->dtype == HILS_BF16) {
-    if (d->head_dim == 64) kv_read_quant_kernel<__nv_bfloat16, 64><<<grid, 256, 0, st>>>(p);
-    else kv_read_quant_kernel<__nv_bfloat16, 128><<<grid, 256, 0, st>>>(p);
+    if (d->head_dim == 64) kv_read_quant_kernel<__nv_bfloat16, 64><<<grid, 128, 0, st>>>(p);
+    else kv_read_quant_kernel<__nv_bfloat16, 128><<<grid, 128, 0, st>>>(p);
   } else {
-    if (d->head_dim == 64) kv_read_quant_kernel<float, 64><<<grid, 256, 0, st>>>(p);
-    else kv_read_quant_kernel<float, 128><<<grid, 256, 0, st>>>(p);
+    if (d->head_dim == 64) kv_read_quant_kernel<float, 64><<<grid, 128, 0, st>>>(p);
+    else kv_read_quant_kernel<float, 128><<<grid, 128, 0, st>>>(p);
   }
   return launched(1);
 }
