@@ -1,8 +1,8 @@
 // Filling and reading a chunk-paged cache: the append of new keys and values
-// with the position rotation applied on the way, the read-back of a 4-bit
-// cache, and the landmark summaries of the chunks that an append completes.
+// with the position rotation applied on the way, and the read-back of a 4-bit
+// cache.
 //
-// All three take the ragged batch of an append: sequence b has the packed
+// Both, and the summaries of summary_append.cuh, take the ragged batch of an append: sequence b has the packed
 // tokens cu[b] .. cu[b+1]-1, which are its positions seqlens[b] - n_b ..
 // seqlens[b] - 1.
 #pragma once
@@ -119,12 +119,17 @@ __device__ __forceinline__ void widen(uint4 w, float (&x)[Vec16<T>::E]) {
 // used for all rows of the warp.  y = x c + x' s' with x' the other element of
 // the pair (another lane's in the half-split style, fetched by a shuffle).
 // The kinds of row are padded to KPI rows each, so that the warp always works
-// on one kind.  HBM-bound for a prompt; kAppendUnroll pieces per lane are in
-// flight at once.  `share` rows per warp: see launch_append.
-constexpr int kAppendUnroll = 4;
+// on one kind.  HBM-bound for a prompt: two pieces per lane are loaded while
+// two are worked on, at 64 registers and 32 warps per SM.  Measured on a 32K
+// prompt of 16 + 2 x 16 heads of 64 dims (407 MB): 80 us, 5.1 TB/s; four
+// pieces without looking ahead 82 us, the same at 72 registers 94 us, four
+// ahead 98 us, warps of 8 steps instead of up to 32 90 us, one CTA per token
+// with the place found by every thread 178 us.
+constexpr int kAppendUnroll = 2;
+constexpr int kAppendSteps = 32;      // of KPI rows, per warp, where tokens abound
 
 template <typename T, int D, bool Q4>
-__global__ void __launch_bounds__(128) kv_append_kernel(AppendParams p) {
+__global__ void __launch_bounds__(128, 8) kv_append_kernel(AppendParams p) {
   constexpr int E = Vec16<T>::E, LPR = D / E, KPI = 32 / LPR, U = kAppendUnroll;
   const int lane = threadIdx.x & 31, sub = lane % LPR, grp = lane / LPR;
   if (blockIdx.x == 0) check_batch(p.tb, threadIdx.x, 128);
@@ -171,8 +176,7 @@ __global__ void __launch_bounds__(128) kv_append_kernel(AppendParams p) {
       }
     }
   }
-  for (int i0 = it0; i0 < it1; i0 += U) {
-    uint4 w[U];
+  auto load = [&](int i0, uint4 (&w)[U]) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int it = i0 + u;
@@ -183,6 +187,12 @@ __global__ void __launch_bounds__(128) kv_append_kernel(AppendParams p) {
       if (it < it1 && h < (kind == 0 ? p.Hq : p.Hkv))
         w[u] = *reinterpret_cast<const uint4*>(static_cast<const T*>(src.data) + t * src.ts + h * src.hs + dim0);
     }
+  };
+  uint4 w[U];
+  load(it0, w);
+  for (int i0 = it0; i0 < it1; i0 += U) {
+    uint4 ahead[U];
+    load(i0 + U, ahead);     // of the next round, while this one is worked on
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int it = i0 + u;
@@ -222,6 +232,8 @@ __global__ void __launch_bounds__(128) kv_append_kernel(AppendParams p) {
       else if (store)
         Vec16<T>::store(static_cast<T*>(pool) + (row * kChunk + in_chunk) * D + dim0, x);
     }
+#pragma unroll
+    for (int u = 0; u < U; ++u) w[u] = ahead[u];
   }
 }
 
@@ -305,118 +317,6 @@ __global__ void __launch_bounds__(128) kv_read_quant_kernel(ReadParams p) {
         } else {
           *reinterpret_cast<float4*>(out + 32 * g) = make_float4(x[0], x[1], x[2], x[3]);
           *reinterpret_cast<float4*>(out + 32 * g + 4) = make_float4(x[4], x[5], x[6], x[7]);
-        }
-      }
-    }
-  }
-}
-
-// A chunk's key rows, in the cache's type or in 4 bits.
-template <typename T, int D> struct DenseRows {
-  static constexpr int E = Vec16<T>::E;
-  static constexpr int64_t BLOCK = int64_t(kChunk) * D * sizeof(T);
-  __device__ __forceinline__ static void load(const uint8_t* block, int row, int sub, float (&x)[E]) {
-    Vec16<T>::load_stream(reinterpret_cast<const T*>(block) + row * D + sub * E, x);
-  }
-};
-template <typename T, int D> struct QuantRows {
-  static constexpr int E = Vec16<T>::E;
-  static constexpr int64_t BLOCK = QuantPage<D>::BLOCK;
-  __device__ __forceinline__ static void load(const uint8_t* block, int row, int sub, float (&x)[E]) {
-    quant_load_row<D, E>(block, row, sub, x);
-  }
-};
-
-struct SummaryParams {
-  TokenBatch tb;
-  const uint8_t* k_pages;
-  const int32_t* table;
-  int64_t n_pages, nc, unit;    // tokens that one warp looks through
-  const void* lq;
-  float *kp, *bp;
-  __nv_bfloat16* kmma;
-  int Hkv;
-  float tau;
-};
-
-// One warp per (`unit` packed tokens, kv head): it summarises each chunk whose
-// last position is among its tokens, as summary_kernel does a chunk.
-template <typename T, int D, typename Rows>
-__global__ void __launch_bounds__(128) summary_append_kernel(SummaryParams p) {
-  constexpr int E = Rows::E, LPK = D / E, KPI = 32 / LPK, ITERS = kChunk / KPI;
-  const int lane = threadIdx.x & 31, grp = lane / LPK, sub = lane % LPK;
-  const int64_t w = (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-  const int64_t n_units = (p.tb.n_tokens + p.unit - 1) / p.unit;
-  if (w >= n_units * p.Hkv) return;
-  const int64_t h = w % p.Hkv, t0 = w / p.Hkv * p.unit;
-  const int64_t t1 = t0 + p.unit < p.tb.n_tokens ? t0 + p.unit : p.tb.n_tokens;
-  if (w == 0) check_batch(p.tb, lane, 32);
-  for (int64_t tt = t0; tt < t1; tt += 32) {
-    Place mine{-1, 0};
-    if (tt + lane < t1) mine = find_place(p.tb, tt + lane);
-    uint32_t todo = __ballot_sync(0xffffffffu, mine.b >= 0 && mine.pos % kChunk == kChunk - 1);
-    while (todo) {
-      const int from = __ffs(int(todo)) - 1;
-      todo &= todo - 1;
-      const int64_t b = __shfl_sync(0xffffffffu, mine.b, from), c = __shfl_sync(0xffffffffu, mine.pos, from) / kChunk;
-      const int64_t page = __ldg(p.table + b * p.nc + c), bh = b * p.Hkv + h;
-      if (page < 0 || page >= p.n_pages) {
-        if (lane == 0) record_error(HILS_ERR_DEVICE_BOUNDS);
-        continue;
-      }
-      const uint8_t* block = p.k_pages + (page * p.Hkv + h) * Rows::BLOCK;
-      float lq[E];
-      Vec16<T>::load(static_cast<const T*>(p.lq) + (bh * p.nc + c) * D + sub * E, lq);
-      float m = -INFINITY, l = 0.f, s = 0.f, acc[E];
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = 0.f;
-#pragma unroll 4
-      for (int it = 0; it < ITERS; ++it) {
-        float k[E];
-        Rows::load(block, it * KPI + grp, sub, k);
-        float part = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) part = fmaf(lq[e], k[e], part);
-        const float z = group_sum<LPK>(part) * p.tau;
-        const float mn = fmaxf(m, z), a = expf(m - mn), q = expf(z - mn);
-        l = l * a + q;
-        s = s * a + q * z;
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = acc[e] * a + q * k[e];
-        m = mn;
-      }
-#pragma unroll
-      for (int off = LPK; off < 32; off <<= 1) {
-        const float mo = __shfl_xor_sync(0xffffffffu, m, off), lo = __shfl_xor_sync(0xffffffffu, l, off);
-        const float so = __shfl_xor_sync(0xffffffffu, s, off);
-        const float mn = fmaxf(m, mo), a = expf(m - mn), q = expf(mo - mn);
-        l = l * a + lo * q;
-        s = s * a + so * q;
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = acc[e] * a + __shfl_xor_sync(0xffffffffu, acc[e], off) * q;
-        m = mn;
-      }
-      if (grp != 0) continue;
-      const float inv = 1.f / l, bias = m + logf(l) - s * inv;
-#pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] *= inv;
-      float* ko = p.kp + (bh * p.nc + c) * D + sub * E;
-#pragma unroll
-      for (int e = 0; e < E; e += 4) *reinterpret_cast<float4*>(ko + e) = make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
-      if (sub == 0) p.bp[bh * p.nc + c] = bias;
-      if (p.kmma != nullptr) {
-        __nv_bfloat16* row = p.kmma + (bh * p.nc + c) * (D + kExt);
-#pragma unroll
-        for (int e = 0; e < E; e += 2)
-          *reinterpret_cast<__nv_bfloat162*>(row + sub * E + e) = __floats2bfloat162_rn(acc[e], acc[e + 1]);
-        if (sub == 0) {
-          // b'/tau as the sum of two bf16 values (see summary_kernel)
-          const float x = bias / p.tau;
-          __nv_bfloat162 hl;
-          hl.x = __float2bfloat16_rn(x);
-          hl.y = __float2bfloat16_rn(x - __bfloat162float(hl.x));
-          *reinterpret_cast<uint4*>(row + D) = make_uint4(*reinterpret_cast<uint32_t*>(&hl), 0u, 0u, 0u);
-          *reinterpret_cast<uint4*>(row + D + 8) = make_uint4(0u, 0u, 0u, 0u);
         }
       }
     }

@@ -8,68 +8,10 @@
 #include <cooperative_groups.h>
 
 #include "decode.cuh"
+#include "mma16.cuh"
 #include "quant.cuh"
 
 namespace hils {
-
-// c += a b for 16x16 a (row) and 16x8 b (column), fp32 sums
-__device__ __forceinline__ void mma16816_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                              uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void mma16816_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                             uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-// transpose of an 8x8 matrix of 16-bit values spread over the warp
-__device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
-  uint32_t d;
-  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
-  return d;
-}
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  const __half2 v = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-// the two bf16 values of a register in fp32
-__device__ __forceinline__ float lo_bf16(uint32_t x) { return __uint_as_float(x << 16); }
-__device__ __forceinline__ float hi_bf16(uint32_t x) { return __uint_as_float(x & 0xFFFF0000u); }
-
-// 2^x.  FAST: without the scaling that keeps results below 2^-126 (weights that small are zero here)
-template <bool FAST>
-__device__ __forceinline__ float pow2(float x) {
-  if constexpr (!FAST) return exp2f(x);
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// Four codes of two 16-bit units as bf16 pairs: 16 + code has the code in
-// bits 3 .. 6.  CENTRE: code - 8 instead, exactly (one subtraction more; the
-// products' sums then do not carry the offset, which fp32 results would feel).
-template <bool CENTRE>
-__device__ __forceinline__ void codes_bf16(uint32_t x, uint32_t (&a)[4]) {
-  a[0] = ((x << 3) & 0x00780078u) | 0x41804180u;
-  a[1] = ((x >> 1) & 0x00780078u) | 0x41804180u;
-  a[2] = ((x >> 5) & 0x00780078u) | 0x41804180u;
-  a[3] = ((x >> 9) & 0x00780078u) | 0x41804180u;
-  if constexpr (CENTRE) {
-    const __nv_bfloat162 c24 = __floats2bfloat162_rn(24.f, 24.f);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a[i]), c24);
-      a[i] = *reinterpret_cast<const uint32_t*>(&v);
-    }
-  }
-}
 
 // ---------------------------------------------------------------- Q1
 // One warp scores 16 chunks against the query heads of a kv head, eight heads

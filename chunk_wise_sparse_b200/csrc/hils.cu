@@ -20,6 +20,7 @@
 #include "backward.cuh"
 #include "backward_mma.cuh"
 #include "append.cuh"
+#include "summary_append.cuh"
 #include "decode_quant.cuh"
 
 using namespace hils;
@@ -876,7 +877,7 @@ template <typename T, int D, bool Q4>
 int launch_append(AppendParams p, cudaStream_t st) {
   constexpr int KPI = 32 / (D / Vec16<T>::E);
   const int steps = (p.q.data ? (p.Hq + KPI - 1) / KPI : 0) + 2 * ((p.Hkv + KPI - 1) / KPI);
-  share_steps(p.tb.n_tokens, steps, 4 * kAppendUnroll, &p.shares, &p.per_share);
+  share_steps(p.tb.n_tokens, steps, kAppendSteps, &p.shares, &p.per_share);
   const int64_t blocks = (p.tb.n_tokens * p.shares + 3) / 4;
   if (blocks >= (int64_t(1) << 31)) return HILS_ERR_UNSUPPORTED;
   kv_append_kernel<T, D, Q4><<<unsigned(blocks), 128, 0, st>>>(p);
@@ -928,11 +929,22 @@ int append_entry(const hils_dims* d, const hils_tokens* tk, const hils_rotary* r
   return d->head_dim == 64 ? launch_append<float, 64, Q4>(p, st) : launch_append<float, 128, Q4>(p, st);
 }
 
-template <typename T, int D, typename Rows>
+template <typename T, int D, bool Q4>
 int launch_summary_append(SummaryParams p, cudaStream_t st) {
   p.tau = 1.f / sqrtf(float(D));
-  const int64_t units = (p.tb.n_tokens + p.unit - 1) / p.unit * p.Hkv;
-  summary_append_kernel<T, D, Rows><<<unsigned((units + 3) / 4), 128, 0, st>>>(p);
+  // several chunks per CTA where that still leaves a few CTAs for every SM
+  while (p.unit >= kChunk && p.unit < kUnitMost &&
+         p.tb.n_tokens / (2 * p.unit) * ((p.Hkv + 3) / 4) >= 12 * int64_t(sm_count()))
+    p.unit *= 2;
+  const int64_t units = (p.tb.n_tokens + p.unit - 1) / p.unit, wide = units * p.Hkv, narrow = units * ((p.Hkv + 3) / 4);
+  if (wide >= (int64_t(1) << 31)) return HILS_ERR_UNSUPPORTED;
+  if constexpr (Q4) {
+    // a chunk per warp where that fills the GPU's warps
+    if (narrow >= 4 * sm_count()) summary_quant_kernel<T, D, 1><<<unsigned(narrow), 128, 0, st>>>(p);
+    else summary_quant_kernel<T, D, 4><<<unsigned(wide), 128, 0, st>>>(p);
+  } else {
+    summary_append_kernel<T, D><<<unsigned(wide), 128, 0, st>>>(p);
+  }
   return launched(1);
 }
 
@@ -958,26 +970,15 @@ int summary_append_entry(const hils_dims* d, const hils_tokens* tk, const void* 
   p.bp = bprime;
   p.kmma = static_cast<__nv_bfloat16*>(kprime_mma);
   p.Hkv = d->heads_kv;
-  // as many tokens as a sequence has on average, up to a chunk: a warp then
+  // as many tokens as a sequence has on average, up to a chunk: a CTA then
   // meets about one completed chunk at most
   const int64_t mean = p.tb.n_tokens / d->batch;
   p.unit = mean < 1 ? 1 : mean > kChunk ? kChunk : mean;
-  if ((p.tb.n_tokens / p.unit + 1) * p.Hkv >= (int64_t(1) << 33)) return HILS_ERR_UNSUPPORTED;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  using bf16 = __nv_bfloat16;
-  if constexpr (Q4) {
-    if (d->dtype == HILS_BF16)
-      return d->head_dim == 64 ? launch_summary_append<bf16, 64, QuantRows<bf16, 64>>(p, st)
-                               : launch_summary_append<bf16, 128, QuantRows<bf16, 128>>(p, st);
-    return d->head_dim == 64 ? launch_summary_append<float, 64, QuantRows<float, 64>>(p, st)
-                             : launch_summary_append<float, 128, QuantRows<float, 128>>(p, st);
-  } else {
-    if (d->dtype == HILS_BF16)
-      return d->head_dim == 64 ? launch_summary_append<bf16, 64, DenseRows<bf16, 64>>(p, st)
-                               : launch_summary_append<bf16, 128, DenseRows<bf16, 128>>(p, st);
-    return d->head_dim == 64 ? launch_summary_append<float, 64, DenseRows<float, 64>>(p, st)
-                             : launch_summary_append<float, 128, DenseRows<float, 128>>(p, st);
-  }
+  if (d->dtype == HILS_BF16)
+    return d->head_dim == 64 ? launch_summary_append<__nv_bfloat16, 64, Q4>(p, st)
+                             : launch_summary_append<__nv_bfloat16, 128, Q4>(p, st);
+  return d->head_dim == 64 ? launch_summary_append<float, 64, Q4>(p, st) : launch_summary_append<float, 128, Q4>(p, st);
 }
 
 struct QuantWs {
