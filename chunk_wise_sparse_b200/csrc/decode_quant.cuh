@@ -211,13 +211,12 @@ quant_topk_kernel(const float* __restrict__ ws_scores, const int32_t* __restrict
 // memory (copies of the next chunk's keys start as soon as the current ones
 // are consumed, its values likewise) and attends it for all heads that kept
 // it at once:
-//   logits (keys x heads): codes are widened to bf16 16 + code (one shift and
-//     one and-or per two codes), multiplied on the tensor cores with the bf16
-//     queries and summed in fp32 per group of 32 dims, starting from -16 times
-//     the group's sum of q, so that acc_jg = sum_{i in g} q_i code_ji; then
+//   logits (keys x heads): the codes, masked out in place as fp16 subnormals
+//     code 2^-24 or code 2^-20 (codes_f16: one and per two codes), times the
+//     queries on the tensor cores, exactly, summed in fp32 per group of 32 dims:
+//     acc_jg = sum_{i in g} q_i code_ji; then
 //     z = tau sum_g [ s_jg acc_jg + m_jg sum_{i in g} q_i ].
-//   output (dims x heads): the codes as they are, fp16 subnormals code 2^-24,
-//     times fp16(w_j s_jg); and m_jg times fp16(w_j), one instruction for all
+//   output (dims x heads): the codes in the same form times fp16(w_j s_jg); and m_jg times fp16(w_j), one instruction for all
 //     groups; w_j = e^(z_j - lse) e^(u - M) carries the fusion weight.  Rounding
 //     the weights to fp16 costs 2^-12 of each, an eighth of a bf16 output's.
 // fp32 models: queries, and the weights times s and m, as sums of three bf16
@@ -248,8 +247,6 @@ quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, co
   using P = QuantPage<D>;
   constexpr int NG = P::G, NS = sizeof(T) == 2 ? 1 : 3;
   constexpr float kLog2e = 1.4426950408889634f;
-  constexpr float OFF = NS == 1 ? 16.f : -8.f;     // what codes_bf16 adds to a code
-  constexpr float kSumScale = 1.f / 256.f;         // of the sums of q in fp16: |q| up to 5e5
   namespace cg = cooperative_groups;
   extern __shared__ __align__(16) uint8_t qsm[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gid = lane >> 2, tig = lane & 3;
@@ -267,50 +264,83 @@ quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, co
   const uint32_t stage_a = uint32_t(__cvta_generic_to_shared(stage));
 
   // queries as the column operand: head gid, dims 32 g + 8 tig + {i, i + 4} in
-  // register i of group g, the order in which two 16-bit units of codes unpack
-  uint32_t qb[NS][NG][4];
-  float qoff[NG][2];      // -OFF x the group's sum of q, heads 2 tig, 2 tig + 1: what the codes' offset adds
-  uint32_t qs2[2] = {0u, 0u};   // NS == 1: the sums as a column operand, see the logits
+  // register i of group g, the order in which two 16-bit units of codes unpack.
+  // NS == 1: in fp16, exact: a head's queries are scaled by a power of two that
+  // puts the largest in [2^14, 2^15) (one 2^-24 of it is lost in the rounding),
+  // and those of odd i by another 2^-4, because their codes stand 2^4 higher
+  uint32_t qb[NS][NG][4], qs2[2] = {0u, 0u};
+  float qsum[NG][2];       // NS == 3: sum of the group's q, heads 2 tig, 2 tig + 1
+  float zscale[2];         // from a logit's sums to the logit x log2 e, heads 2 tig, 2 tig + 1
   {
     const T* qr = q + (row0 + (gid < GV ? gid : 0)) * D + 8 * tig;
+    float x[NG][8], top = 0.f;
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-      float x[8];
       if constexpr (NS == 1) {
-        Vec16<T>::load(qr + 32 * g, x);
+        Vec16<T>::load(qr + 32 * g, x[g]);
       } else {
         float y[4], z[4];
         Vec16<T>::load(qr + 32 * g, y);
         Vec16<T>::load(qr + 32 * g + 4, z);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) { x[e] = y[e]; x[e + 4] = z[e]; }
+        for (int e = 0; e < 4; ++e) { x[g][e] = y[e]; x[g][e + 4] = z[e]; }
       }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (gid >= GV) x[g][e] = 0.f;
+        top = fmaxf(top, fabsf(x[g][e]));
+      }
+    }
+    float up = 1.f, down = 1.f;
+    if constexpr (NS == 1) {
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // exponent e of the largest (biased): scale by 2^(141 - e), within fp32's normal powers
+      int e = int(__float_as_uint(top) >> 23);
+      e = e < 30 ? 30 : e > 250 ? 250 : e;
+      up = __uint_as_float(uint32_t(268 - e) << 23);      // 2^(141 - e)
+      down = __uint_as_float(uint32_t(e - 14) << 23);     // 2^(e - 141)
+    }
+    zscale[0] = tau * kLog2e * __shfl_sync(0xffffffffu, down, 8 * tig);
+    zscale[1] = tau * kLog2e * __shfl_sync(0xffffffffu, down, 8 * tig + 4);
+    if constexpr (NS == 1) {     // codes were multiplied as code 2^-24
+      zscale[0] *= 16777216.f;
+      zscale[1] *= 16777216.f;
+    }
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
       float s = 0.f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        if (gid >= GV) x[e] = 0.f;
-        s += x[e];
+        x[g][e] *= up;
+        s += x[g][e];
       }
-#pragma unroll
-      for (int n = 0; n < NS; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t r = pack_bf16(x[i], x[i + 4]);
-          qb[n][g][i] = r;
-          x[i] -= lo_bf16(r);
-          x[i + 4] -= hi_bf16(r);
-        }
       s += __shfl_xor_sync(0xffffffffu, s, 1);
       s += __shfl_xor_sync(0xffffffffu, s, 2);
-      qoff[g][0] = -OFF * __shfl_sync(0xffffffffu, s, 8 * tig);
-      qoff[g][1] = -OFF * __shfl_sync(0xffffffffu, s, 8 * tig + 4);
       if constexpr (NS == 1) {
-        // rows 2 tig, 2 tig + 1 (groups) in fp16, rows + 8 what that rounds off
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float f = i & 1 ? 0.0625f : 1.f;
+          qb[0][g][i] = pack_f16(x[g][i] * f, x[g][i + 4] * f);
+        }
+        // the groups' sums x 2^-8, rows 2 tig, 2 tig + 1 in fp16, rows + 8 what that rounds off
         if (g / 2 == tig) {
-          const float v = s * kSumScale, r = v - __half2float(__float2half_rn(v));
+          const float v = s * (1.f / 256.f), r = v - __half2float(__float2half_rn(v));
           qs2[0] |= pack_f16(v, 0.f) << (16 * (g % 2));
           qs2[1] |= pack_f16(r, 0.f) << (16 * (g % 2));
         }
+      } else {
+        qsum[g][0] = __shfl_sync(0xffffffffu, s, 8 * tig);
+        qsum[g][1] = __shfl_sync(0xffffffffu, s, 8 * tig + 4);
+#pragma unroll
+        for (int n = 0; n < NS; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t r = pack_bf16(x[g][i], x[g][i + 4]);
+            qb[n][g][i] = r;
+            x[g][i] -= lo_bf16(r);
+            x[g][i + 4] -= hi_bf16(r);
+          }
       }
     }
   }
@@ -441,7 +471,7 @@ quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, co
     float z[4][4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      uint32_t cw[2][NG];      // the lane's two units of each group, one register each, for the two rows
+      uint32_t cu[2][NG];      // the lane's code words of the two rows: units of 2 tig, then of 2 tig + 1
       float ps[2][NG], pm[2][NG];
       uint32_t la[2];          // NS == 1: least values of groups 2 tig, 2 tig + 1
 #pragma unroll
@@ -450,14 +480,10 @@ quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, co
         const uint8_t* par = stage + P::param_off(key);
         if constexpr (NG == 4) {
           const uint4 u = *reinterpret_cast<const uint4*>(stage + P::code_off(key) + 16 * tig);
-          cw[r][0] = __byte_perm(u.x, u.z, 0x5410);
-          cw[r][1] = __byte_perm(u.x, u.z, 0x7632);
-          cw[r][2] = __byte_perm(u.y, u.w, 0x5410);
-          cw[r][3] = __byte_perm(u.y, u.w, 0x7632);
+          cu[r][0] = u.x; cu[r][1] = u.y; cu[r][2] = u.z; cu[r][3] = u.w;
         } else {
           const uint2 u = *reinterpret_cast<const uint2*>(stage + P::code_off(key) + 8 * tig);
-          cw[r][0] = __byte_perm(u.x, u.y, 0x5410);
-          cw[r][1] = __byte_perm(u.x, u.y, 0x7632);
+          cu[r][0] = u.x; cu[r][1] = u.y;
         }
         if constexpr (NS == 1) {
           const uint2 m = *reinterpret_cast<const uint2*>(par + 8 * (tig % (NG / 2)));
@@ -476,23 +502,33 @@ quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, co
       if constexpr (NS == 1) mma16816_f16(z[t], la[0], la[1], la[0], la[1], qs2[0], qs2[1]);
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
+        float c[4] = {0.f, 0.f, 0.f, 0.f};
         uint32_t a[2][4];
-        codes_bf16<NS == 3>(cw[0][g], a[0]);
-        codes_bf16<NS == 3>(cw[1][g], a[1]);
-        float c[4] = {qoff[g][0], qoff[g][1], qoff[g][0], qoff[g][1]};
 #pragma unroll
-        for (int n = NS - 1; n >= 0; --n) {
-          mma16816_bf16(c, a[0][0], a[1][0], a[0][1], a[1][1], qb[n][g][0], qb[n][g][1]);
-          mma16816_bf16(c, a[0][2], a[1][2], a[0][3], a[1][3], qb[n][g][2], qb[n][g][3]);
+        for (int r = 0; r < 2; ++r) {
+          if constexpr (NS == 1) codes_f16(cu[r][g / 2], cu[r][NG / 2 + g / 2], g & 1, a[r]);
+          else codes_bf16<true>(__byte_perm(cu[r][g / 2], cu[r][NG / 2 + g / 2], g & 1 ? 0x7632 : 0x5410), a[r]);
+        }
+        if constexpr (NS == 1) {
+          mma16816_f16(c, a[0][0], a[1][0], a[0][1], a[1][1], qb[0][g][0], qb[0][g][1]);
+          mma16816_f16(c, a[0][2], a[1][2], a[0][3], a[1][3], qb[0][g][2], qb[0][g][3]);
+        } else {
+#pragma unroll
+          for (int n = NS - 1; n >= 0; --n) {
+            mma16816_bf16(c, a[0][0], a[1][0], a[0][1], a[1][1], qb[n][g][0], qb[n][g][1]);
+            mma16816_bf16(c, a[0][2], a[1][2], a[0][3], a[1][3], qb[n][g][2], qb[n][g][3]);
+          }
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          if constexpr (NS == 1) z[t][i] = g == 0 ? fmaf(z[t][i], 1.f / kSumScale, ps[i / 2][g] * c[i]) : fmaf(ps[i / 2][g], c[i], z[t][i]);
-          else z[t][i] = fmaf(ps[i / 2][g], c[i], fmaf(pm[i / 2][g], qoff[g][i % 2] * (-1.f / OFF), z[t][i]));
+          if constexpr (NS == 1)     // the least values' sum in the codes' units: 2^8 / 2^24
+            z[t][i] = g == 0 ? fmaf(z[t][i], 1.f / 65536.f, ps[i / 2][g] * c[i]) : fmaf(ps[i / 2][g], c[i], z[t][i]);
+          else
+            z[t][i] = fmaf(ps[i / 2][g], c[i], fmaf(fmaf(8.f, ps[i / 2][g], pm[i / 2][g]), qsum[g][i % 2], z[t][i]));
         }
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) z[t][i] *= tau * kLog2e;
+      for (int i = 0; i < 4; ++i) z[t][i] *= zscale[i & 1];
     }
     if (cur.keys < kChunk) {       // the own chunk: keys behind the query
 #pragma unroll
@@ -595,9 +631,6 @@ quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, co
         mma16816_f16(lm, __byte_perm(vl[0][0], vl[0][1], 0x7632), 0u, __byte_perm(vl[1][0], vl[1][1], 0x7632), 0u, wb[0], wb[1]);
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
-        uint32_t x[2];       // units of the two keys of each half side by side
-#pragma unroll
-        for (int r = 0; r < 2; ++r) x[r] = __byte_perm(vc[r][0][g / 2], vc[r][1][g / 2], g & 1 ? 0x7632 : 0x5410);
         if constexpr (NS == 1) {
           uint32_t bs[2];
 #pragma unroll
@@ -606,10 +639,11 @@ quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, co
             const __half2 ws = __hmul2(*reinterpret_cast<const __half2*>(&wb[r]), *reinterpret_cast<const __half2*>(&s2));
             bs[r] = *reinterpret_cast<const uint32_t*>(&ws) & kept_mask;
           }
-          mma16816_f16(acc[g][0], x[0] & 0x000F000Fu, (x[0] >> 4) & 0x000F000Fu, x[1] & 0x000F000Fu,
-                       (x[1] >> 4) & 0x000F000Fu, bs[0], bs[1]);
-          mma16816_f16(acc[g][1], (x[0] >> 8) & 0x000F000Fu, (x[0] >> 12) & 0x000F000Fu, (x[1] >> 8) & 0x000F000Fu,
-                       (x[1] >> 12) & 0x000F000Fu, bs[0], bs[1]);
+          uint32_t a[2][4];       // codes of dims 32 g + 4 gid + i, the two keys of each half side by side
+#pragma unroll
+          for (int r = 0; r < 2; ++r) codes_f16(vc[r][0][g / 2], vc[r][1][g / 2], g & 1, a[r]);
+          mma16816_f16(acc[g][0], a[0][0], a[0][1], a[1][0], a[1][1], bs[0], bs[1]);
+          mma16816_f16(acc[g][1], a[0][2], a[0][3], a[1][2], a[1][3], bs[0], bs[1]);
         } else {
           // w s and w (m + 8 s) as sums of three bf16 values, the latter through
           // rows of ones
@@ -620,11 +654,12 @@ quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, co
             for (int j = 0; j < 2; ++j) {
               const float2 sm = __half22float2(*reinterpret_cast<const __half2*>(&vp[r][j][g]));
               fs[r][j] = kept_mask ? wf[r][j] * sm.x : 0.f;
-              fm[r][j] = kept_mask ? wf[r][j] * fmaf(-OFF, sm.x, sm.y) : 0.f;
+              fm[r][j] = kept_mask ? wf[r][j] * fmaf(8.f, sm.x, sm.y) : 0.f;
             }
           uint32_t a[2][4];
-          codes_bf16<true>(x[0], a[0]);
-          codes_bf16<true>(x[1], a[1]);
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+            codes_bf16<true>(__byte_perm(vc[r][0][g / 2], vc[r][1][g / 2], g & 1 ? 0x7632 : 0x5410), a[r]);
           // fresh sums per tile, added in fp32: the matrix unit's own sums are not rounded to nearest
           float c0[4] = {0.f, 0.f, 0.f, 0.f}, c1[4] = {0.f, 0.f, 0.f, 0.f}, cm[4] = {0.f, 0.f, 0.f, 0.f};
           constexpr uint32_t one = 0x3F803F80u;
@@ -664,15 +699,16 @@ quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, co
   for (int g = 0; g < NG; ++g)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      float add = 0.f, f = 1.f;
+      float add = 0.f, f = 1.f, f4 = 1.f;
       if constexpr (NS == 1) {
         add = __shfl_sync(0xffffffffu, least[e], 4 * g + tig);
-        f = 16777216.f;      // the codes were multiplied as code 2^-24
+        f = 16777216.f;      // the codes were multiplied as code 2^-24, those of rows gid + 8 (odd dims) as code 2^-20
+        f4 = 1048576.f;
       }
       // dims 32 g + 4 gid + 0 .. 3
       *reinterpret_cast<float4*>(mine + (2 * tig + e) * A::RS + 32 * g + 4 * gid) =
-          make_float4(fmaf(acc[g][0][e], f, add), fmaf(acc[g][0][2 + e], f, add), fmaf(acc[g][1][e], f, add),
-                      fmaf(acc[g][1][2 + e], f, add));
+          make_float4(fmaf(acc[g][0][e], f, add), fmaf(acc[g][0][2 + e], f4, add), fmaf(acc[g][1][e], f, add),
+                      fmaf(acc[g][1][2 + e], f4, add));
     }
   if (gid == 0)
 #pragma unroll

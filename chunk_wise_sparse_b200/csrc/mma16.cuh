@@ -49,6 +49,18 @@ __device__ __forceinline__ float pow2(float x) {
   return y;
 }
 
+// The four codes of a 16-bit unit of x and of one of y (the upper ones if
+// `upper`), side by side, as fp16 subnormals: code 0 in bits 0 .. 3 is
+// code 2^-24, code 1 left in bits 4 .. 7 is code 2^-20, and codes 2 and 3
+// likewise after a byte's move, which costs nothing in the permutation.
+__device__ __forceinline__ void codes_f16(uint32_t x, uint32_t y, bool upper, uint32_t (&a)[4]) {
+  const uint32_t lo = __byte_perm(x, y, upper ? 0x7632 : 0x5410), hi = __byte_perm(x, y, upper ? 0x7733 : 0x5511);
+  a[0] = lo & 0x000F000Fu;
+  a[1] = lo & 0x00F000F0u;
+  a[2] = hi & 0x000F000Fu;
+  a[3] = hi & 0x00F000F0u;
+}
+
 // Four codes of two 16-bit units as bf16 pairs: 16 + code has the code in
 // bits 3 .. 6.  CENTRE: code - 8 instead, exactly (one subtraction more; the
 // products' sums then do not carry the offset, which fp32 results would feel).
