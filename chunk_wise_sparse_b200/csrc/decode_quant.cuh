@@ -72,49 +72,83 @@ quant_scores_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __
 }
 
 // ---------------------------------------------------------------- Q2
-// The K largest scores of a row by bisection of the K-th largest order key:
-// count the keys at or above a threshold until exactly K are, or the interval
-// closes on a tied value, whose lowest ids are taken.  A count costs a few
-// instructions per key and one barrier, and the exit comes after about
-// log2(key range / gap at the K-th score) steps, ten or so; a radix select
+// Exclusive prefix sum over the NT threads of a block; also the total.
+template <int NT>
+__device__ __forceinline__ int block_exclusive_scan(int x, int* warp_tot, int& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int incl = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  __syncthreads();
+  if (lane == 31) warp_tot[warp] = incl;
+  __syncthreads();
+  // the warps' totals, summed by every warp
+  const int t = lane < NT / 32 ? warp_tot[lane] : 0;
+  total = __reduce_add_sync(0xffffffffu, t);
+  return __reduce_add_sync(0xffffffffu, lane < warp ? t : 0) + incl - x;
+}
+
+// A kept (head, slot) pair: chunk id (-1: none), page (-1: outside the pool),
+// score.
+struct __align__(16) Kept {
+  int32_t id, page;
+  float score;
+  int32_t pad;
+};
+
+// The K largest scores of a row by bisection: count the keys at or above a
+// threshold until exactly K are, or the interval closes on a tied value, whose
+// lowest ids are taken.  A count costs a few instructions per key and one
+// barrier, and the exit comes after about log2(range of the scores / gap at the
+// K-th) steps, ten or so; a radix select
 // instead sends all of a row's scores, which share their high bits, through
-// atomics on a few shared counters.  Each thread holds a contiguous segment of
-// keys in registers (IT = 0: re-read from L2), so the ids come out ascending.
-template <int IT>
-__global__ void __launch_bounds__(256)
+// atomics on a few shared counters.  Each of the NT threads holds a contiguous
+// segment of IT keys in registers (IT = 0: re-read from L2), so the ids come
+// out ascending.  A kept chunk's page is looked up here, by the thread that
+// keeps it.
+template <int IT, int NT>
+__global__ void __launch_bounds__(NT)
 quant_topk_kernel(const float* __restrict__ ws_scores, const int32_t* __restrict__ seqlens, int64_t cap, int64_t nc,
-                  int Hq, int K, int32_t* __restrict__ sel_ids, float* __restrict__ sel_scores,
+                  int Hq, int K, const int32_t* __restrict__ table, int64_t n_pages, Kept* __restrict__ kept,
                   int32_t* __restrict__ ids_out, float* __restrict__ scores_out, int wm1) {
-  __shared__ __align__(16) uint32_t s_part[2][8];
-  __shared__ uint32_t s_min[8], s_max[8];
-  __shared__ int warp_tot[8];
+  constexpr int NW = NT / 32;
+  __shared__ uint32_t s_part[2][32], s_min[32], s_max[32];
+  __shared__ int warp_tot[32];
   pdl_wait();      // the scores
   pdl_trigger();
-  const int row = blockIdx.x, b = row / Hq, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t own = decode_own_chunk(seqlens, b, cap);
+  const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t b = row / Hq, own = decode_own_chunk(seqlens, int(b), cap);
   int64_t n = own < 0 ? 0 : own - wm1;   // candidates
   if (n < 0) n = 0;
   const float* sc = ws_scores + int64_t(row) * nc;
   const int64_t at = int64_t(row) * K;
   auto put = [&](int slot, int32_t id, float s) {
-    sel_ids[at + slot] = id;
-    sel_scores[at + slot] = s;
     if (ids_out) ids_out[at + slot] = id;
     if (scores_out) scores_out[at + slot] = s;
+    int32_t page = -1;
+    if (id >= 0) {
+      page = __ldg(table + b * nc + id);
+      if (page < 0 || page >= n_pages) {
+        record_error(HILS_ERR_DEVICE_BOUNDS);
+        page = -1;
+      }
+    }
+    kept[at + slot] = Kept{id, page, s, 0};
   };
   if (n <= K) {
-    for (int t = tid; t < K; t += 256) put(t, t < n ? t : -1, t < n ? sc[t] : -INFINITY);
+    for (int t = tid; t < K; t += NT) put(t, t < n ? t : -1, t < n ? sc[t] : -INFINITY);
     return;
   }
-  const int64_t seg = IT > 0 && IT % 4 == 0 ? ((n + 255) / 256 + 3) / 4 * 4 : (n + 255) / 256;
+  const int64_t seg = IT > 0 ? ((n + NT - 1) / NT + 3) / 4 * 4 : (n + NT - 1) / NT;
   const int64_t s0 = tid * seg;
   const int64_t cnt = s0 >= n ? 0 : (s0 + seg <= n ? seg : n - s0);
   constexpr int R = IT > 0 ? IT : 1;
   uint32_t key[R];
   if constexpr (IT > 0) {
-    // rows of scores start 256-byte aligned when nc is a multiple of 64, else
-    // at any multiple of 4 bytes
-    const bool vec = (nc & 3) == 0;
+    const bool vec = (nc & 3) == 0;      // every row of scores starts on a 16-byte boundary
 #pragma unroll
     for (int e = 0; e < IT; e += 4) {
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -139,7 +173,7 @@ quant_topk_kernel(const float* __restrict__ ws_scores, const int32_t* __restrict
 #pragma unroll
       for (int e = 0; e < IT; ++e) f(key[e]);
     } else {
-      for (int64_t c = tid; c < n; c += 256) f(max(order_key(sc[c]), 1u));
+      for (int64_t c = tid; c < n; c += NT) f(max(order_key(sc[c]), 1u));
     }
   };
   uint32_t lo = 0xFFFFFFFFu, hi = 0u;
@@ -151,8 +185,8 @@ quant_topk_kernel(const float* __restrict__ ws_scores, const int32_t* __restrict
   hi = __reduce_max_sync(0xffffffffu, hi);
   if (lane == 0) { s_min[warp] = lo; s_max[warp] = hi; }
   __syncthreads();
-#pragma unroll
-  for (int w = 0; w < 8; ++w) { lo = min(lo, s_min[w]); hi = max(hi, s_max[w]); }
+  lo = __reduce_min_sync(0xffffffffu, lane < NW ? s_min[lane] : 0xFFFFFFFFu);
+  hi = __reduce_max_sync(0xffffffffu, lane < NW ? s_max[lane] : 0u);
   int flip = 0;
   auto count = [&](uint32_t t) {   // keys >= t of the whole row
     uint32_t x = 0;
@@ -160,14 +194,22 @@ quant_topk_kernel(const float* __restrict__ ws_scores, const int32_t* __restrict
     x = __reduce_add_sync(0xffffffffu, x);
     if (lane == 0) s_part[flip][warp] = x;
     __syncthreads();
-    const uint4 p0 = *reinterpret_cast<const uint4*>(s_part[flip]), p1 = *reinterpret_cast<const uint4*>(s_part[flip] + 4);
+    x = lane < NW ? s_part[flip][lane] : 0u;
     flip ^= 1;
-    return int(p0.x + p0.y + p0.z + p0.w + p1.x + p1.y + p1.z + p1.w);
+    return int(__reduce_add_sync(0xffffffffu, x));
   };
   // the largest t with at least K keys >= t, or any t with exactly K
   bool exact = false;
-  while (lo < hi) {
-    const uint32_t d = hi - lo, mid = lo + (d >> 1) + (d & 1);
+  auto value = [](uint32_t k) { return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k); };
+  for (int step = 0; lo < hi; ++step) {
+    const uint32_t d = hi - lo;
+    uint32_t mid = lo + (d >> 1) + (d & 1);
+    // halve the scores' interval first: the keys' is nine tenths exponents of
+    // scores near zero
+    if (step < 16) {
+      const uint32_t k = order_key(0.5f * value(lo) + 0.5f * value(hi));
+      if (k > lo && k <= hi) mid = k;
+    }
     const int c = count(mid);
     if (c >= K) lo = mid; else hi = mid - 1;
     if (c == K) { exact = true; break; }
@@ -175,7 +217,7 @@ quant_topk_kernel(const float* __restrict__ ws_scores, const int32_t* __restrict
   const int ties = exact || lo == 0xFFFFFFFFu ? K : K - count(lo + 1);   // how many keys equal to lo are kept
   // each thread's keys above lo, and equal to it, in chunk order
   int gt = 0, eq = 0;
-  auto at_key = [&](int64_t e) { return IT > 0 ? 0u : max(order_key(sc[s0 + e]), 1u); };
+  auto at_key = [&](int64_t e) { return max(order_key(sc[s0 + e]), 1u); };
   if constexpr (IT > 0) {
 #pragma unroll
     for (int e = 0; e < IT; ++e) { gt += key[e] > lo; eq += key[e] == lo; }
@@ -185,20 +227,28 @@ quant_topk_kernel(const float* __restrict__ ws_scores, const int32_t* __restrict
   int tot;
   int take_eq = eq;
   if (!exact) {
-    take_eq = ties - block_exclusive_scan256(eq, warp_tot, tot);
+    take_eq = ties - block_exclusive_scan<NT>(eq, warp_tot, tot);
     take_eq = take_eq < 0 ? 0 : (take_eq > eq ? eq : take_eq);
   }
-  int pos = block_exclusive_scan256(gt + take_eq, warp_tot, tot);
+  int pos = block_exclusive_scan<NT>(gt + take_eq, warp_tot, tot);
   auto emit = [&](int64_t e, uint32_t k) {
     bool take = k > lo;
     if (k == lo) take = take_eq-- > 0;
-    if (take && pos < K) { put(pos, int32_t(s0 + e), sc[s0 + e]); ++pos; }
+    // the score is the key's image undone
+    if (take && pos < K) put(pos++, int32_t(s0 + e), value(k));
   };
   if (gt + take_eq == 0) return;
   if constexpr (IT > 0) {
+#pragma unroll 1
+    for (int e0 = 0; e0 < IT; e0 += 4) {
 #pragma unroll
-    for (int e = 0; e < IT; ++e)
-      if (key[e] >= lo && e < cnt) emit(e, key[e]);
+      for (int i = 0; i < IT; i += 4)
+        if (i == e0) {
+#pragma unroll
+          for (int e = i; e < i + 4; ++e)
+            if (key[e] >= lo) emit(e, key[e]);
+        }
+    }
   } else {
     for (int64_t e = 0; e < cnt; ++e) emit(e, at_key(e));
   }
@@ -233,16 +283,16 @@ template <int D> struct QuantAttend {
   static constexpr int LISTS = 8 * kMaxTopK;                  // kept (head, slot) pairs of a cluster, at most
   static constexpr int ITEMS = LISTS + 16;                    // distinct chunks and window chunks
   // staging, the CTA's sums, scores of the pairs, places of a pair's chunk in
-  // the heads' lists, ids of the pairs, then the items' page and pair
-  static constexpr int SMEM = kQdWarps * STAGE + MERGE + LISTS * 4 + LISTS * 8 + LISTS * 4 + ITEMS * 8;
+  // the heads' lists, ids and pages of the pairs, then the items' page and pair
+  static constexpr int SMEM = kQdWarps * STAGE + MERGE + LISTS * (4 + 8 + 4 + 4) + ITEMS * 8;
 };
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kQdWarps * 32, 2)
 quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, const uint8_t* __restrict__ vpg,
                     const int32_t* __restrict__ table, int64_t n_pages, const int32_t* __restrict__ seqlens,
-                    int64_t cap, int Hq, int G, int Hkv, int K, float tau, const int32_t* __restrict__ sel_ids,
-                    const float* __restrict__ sel_scores, T* __restrict__ o, int n_oct, int wm1) {
+                    int64_t cap, int Hq, int G, int Hkv, int K, float tau, const Kept* __restrict__ kept,
+                    T* __restrict__ o, int n_oct, int wm1) {
   using A = QuantAttend<D>;
   using P = QuantPage<D>;
   constexpr int NG = P::G, NS = sizeof(T) == 2 ? 1 : 3;
@@ -259,7 +309,8 @@ quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, co
   float* scs = reinterpret_cast<float*>(qsm + kQdWarps * A::STAGE + A::MERGE);     // [GV][K], x log2 e
   uint8_t* spot = reinterpret_cast<uint8_t*>(scs + A::LISTS);                       // [pair][8 heads]: slot, 0xFF: not kept
   int32_t* ids = reinterpret_cast<int32_t*>(spot + A::LISTS * 8);                   // [GV][K]
-  int2* items = reinterpret_cast<int2*>(ids + A::LISTS);                            // (page, pair; -1 - w: window chunk w)
+  int32_t* pages = ids + A::LISTS;
+  int2* items = reinterpret_cast<int2*>(pages + A::LISTS);                            // (page, pair; -1 - w: window chunk w)
   __shared__ int s_count[kQdWarps];
   const uint32_t stage_a = uint32_t(__cvta_generic_to_shared(stage));
 
@@ -349,11 +400,22 @@ quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, co
   const int64_t n_cand = own - wm1 > 0 ? own - wm1 : 0;
   const int n_sel = own < 0 ? 0 : GV * K;
   const int n_win = own < 0 ? 0 : int(own < wm1 ? own + 1 : wm1 + 1);
-  pdl_wait();      // the top-K lists
   constexpr int TH = kQdWarps * 32;
+  // the window's pages do not depend on the selection
+  int win_page = -1;
+  if (tid < n_win) {
+    win_page = __ldg(table + b * nc + own - tid);
+    if (win_page < 0 || win_page >= n_pages) {
+      record_error(HILS_ERR_DEVICE_BOUNDS);
+      win_page = -1;
+    }
+  }
+  pdl_wait();      // the top-K lists
   for (int i = tid; i < n_sel; i += TH) {
-    ids[i] = sel_ids[row0 * K + i];
-    scs[i] = sel_scores[row0 * K + i] * kLog2e;
+    const int4 k = __ldg(reinterpret_cast<const int4*>(kept + row0 * K + i));
+    ids[i] = k.x;
+    pages[i] = k.y;
+    scs[i] = __int_as_float(k.z) * kLog2e;
   }
   for (int i = tid; i < n_sel * 2; i += TH) reinterpret_cast<uint32_t*>(spot)[i] = 0xFFFFFFFFu;
   __syncthreads();
@@ -386,24 +448,12 @@ quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, co
     }
   }
   __syncthreads();
-  // the items: pairs that own their chunk, in order, then the window's chunks
+  // the items: the window's chunks, then the pairs that own their chunk
   int n_items = 0;
   for (int p0 = 0; p0 < n_sel + n_win; p0 += TH) {
-    const int pair = p0 + tid;
-    int64_t c = -1;
-    if (pair < n_sel) {
-      if (spot[pair * 8 + pair / K] != 0xFF) c = ids[pair];
-    } else if (pair < n_sel + n_win) {
-      c = own - (pair - n_sel);
-    }
-    int page = -1;
-    if (c >= 0) {
-      page = __ldg(table + b * nc + c);
-      if (page < 0 || page >= n_pages) {
-        record_error(HILS_ERR_DEVICE_BOUNDS);
-        page = -1;
-      }
-    }
+    // the window's chunks first (their items are found without the selection)
+    const int pair = p0 + tid - n_win;
+    const int page = pair < 0 ? win_page : pair < n_sel && spot[pair * 8 + pair / K] != 0xFF ? pages[pair] : -1;
     const uint32_t have = __ballot_sync(0xffffffffu, page >= 0);
     if (lane == 0) s_count[warp] = __popc(have);
     __syncthreads();
@@ -413,7 +463,7 @@ quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, co
       if (w < warp) at += s_count[w];
       n_items += s_count[w];
     }
-    if (page >= 0) items[at] = make_int2(page, pair < n_sel ? pair : -1 - (pair - n_sel));
+    if (page >= 0) items[at] = make_int2(page, pair >= 0 ? pair : -1 - tid);
     __syncthreads();
   }
 

@@ -983,8 +983,7 @@ int summary_append_entry(const hils_dims* d, const hils_tokens* tk, const void* 
 
 struct QuantWs {
   float* scores;      // [B*Hq, nc]
-  int32_t* ids;       // [B*Hq, K]
-  float* sel;         // [B*Hq, K]
+  Kept* kept;         // [B*Hq, K]
 };
 
 size_t quant_ws_layout(const hils_dims* d, char* base, QuantWs* ws) {
@@ -992,9 +991,8 @@ size_t quant_ws_layout(const hils_dims* d, char* base, QuantWs* ws) {
   size_t off = 0;
   auto take = [&](size_t bytes) { char* p = base ? base + off : nullptr; off += align256(bytes); return p; };
   char* a = take(sizeof(float) * rows * size_t(d->seqlen / kChunk));
-  char* b = take(sizeof(int32_t) * rows * d->topk);
-  char* c = take(sizeof(float) * rows * d->topk);
-  if (ws) *ws = QuantWs{reinterpret_cast<float*>(a), reinterpret_cast<int32_t*>(b), reinterpret_cast<float*>(c)};
+  char* b = take(sizeof(Kept) * rows * d->topk);
+  if (ws) *ws = QuantWs{reinterpret_cast<float*>(a), reinterpret_cast<Kept*>(b)};
   return off;
 }
 
@@ -1021,14 +1019,16 @@ int launch_decode_quant(const hils_dims* d, const void* q, const void* q_score, 
                                      kDecChunksPerCta, smem1, st>>>(qs, kp, bp, nullptr, seqlens, d->seqlen, nc,
                                                                     d->heads_q, G, d->heads_kv, tau, ws.scores, wm1);
   }
-  auto topk = [&](auto* fn) {
-    return launch_pdl(fn, dim3(unsigned(rows)), 256, 0, st, static_cast<const float*>(ws.scores), seqlens, d->seqlen, nc,
-                      d->heads_q, K, ws.ids, ws.sel, ids_out, scores_out, wm1);
+  const auto* kpool = static_cast<const uint8_t*>(kpg);
+  const auto* vpool = static_cast<const uint8_t*>(vpg);
+  auto topk = [&](auto* fn, int threads) {
+    return launch_pdl(fn, dim3(unsigned(rows)), threads, 0, st, static_cast<const float*>(ws.scores), seqlens, d->seqlen,
+                      nc, int(d->heads_q), K, table, n_pages, ws.kept, ids_out, scores_out, wm1);
   };
-  cudaError_t e = nc <= 256 * 8    ? topk(quant_topk_kernel<8>)
-                  : nc <= 256 * 32 ? topk(quant_topk_kernel<32>)
-                  : nc <= 256 * 96 ? topk(quant_topk_kernel<96>)
-                                   : topk(quant_topk_kernel<0>);
+  cudaError_t e = nc <= 256 * 8     ? topk(quant_topk_kernel<8, 256>, 256)
+                  : nc <= 1024 * 8  ? topk(quant_topk_kernel<8, 1024>, 1024)
+                  : nc <= 1024 * 32 ? topk(quant_topk_kernel<32, 1024>, 1024)
+                                    : topk(quant_topk_kernel<0, 1024>, 1024);
   if (e != cudaSuccess) return HILS_ERR_CUDA;
   constexpr auto k3 = quant_attend_kernel<T, D>;
   if (set_smem_max<k3>() != cudaSuccess) return HILS_ERR_CUDA;
@@ -1051,9 +1051,8 @@ int launch_decode_quant(const hils_dims* d, const void* q, const void* q_score, 
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, k3, static_cast<const T*>(q), static_cast<const uint8_t*>(kpg),
-                         static_cast<const uint8_t*>(vpg), table, n_pages, seqlens, d->seqlen, int(d->heads_q), G,
-                         int(d->heads_kv), K, tau, static_cast<const int32_t*>(ws.ids), static_cast<const float*>(ws.sel),
+  e = cudaLaunchKernelEx(&cfg, k3, static_cast<const T*>(q), kpool, vpool, table, n_pages, seqlens, d->seqlen,
+                         int(d->heads_q), G, int(d->heads_kv), K, tau, static_cast<const Kept*>(ws.kept),
                          static_cast<T*>(o), n_oct, wm1);
   if (e != cudaSuccess) return HILS_ERR_CUDA;
   return launched(3);
