@@ -280,11 +280,14 @@ template <int D> struct QuantAttend {
   static constexpr int RS = D + 4;                            // floats per merged row: 16-byte stores of four rows apart
   static constexpr int MERGE = 8 * RS * 4 + 8 * 2 * 4;        // per warp: 8 rows, then (maximum, sum) of 8 heads
   static constexpr int STAGE = 2 * BLOCK > MERGE ? 2 * BLOCK : (MERGE + 15) / 16 * 16;
+  // a CTA's sums of one head: D values, maximum, sum; up to 15 arrive at the CTA
+  // that finishes some of eight heads in a cluster of up to eight
+  static constexpr int PART = D + 4, INBOX = 15 * PART;
   static constexpr int LISTS = 8 * kMaxTopK;                  // kept (head, slot) pairs of a cluster, at most
   static constexpr int ITEMS = LISTS + 16;                    // distinct chunks and window chunks
-  // staging, the CTA's sums, scores of the pairs, places of a pair's chunk in
-  // the heads' lists, ids and pages of the pairs, then the items' page and pair
-  static constexpr int SMEM = kQdWarps * STAGE + MERGE + LISTS * (4 + 8 + 4 + 4) + ITEMS * 8;
+  // staging, the CTAs' sums of the heads this one finishes, scores of the pairs, places of a pair's chunk in
+  // the heads' lists, ids of the pairs, then the items' page and pair
+  static constexpr int SMEM = kQdWarps * STAGE + INBOX * 4 + LISTS * (4 + 8 + 4) + ITEMS * 8;
 };
 
 template <typename T, int D>
@@ -299,19 +302,19 @@ quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, co
   constexpr float kLog2e = 1.4426950408889634f;
   namespace cg = cooperative_groups;
   extern __shared__ __align__(16) uint8_t qsm[];
+  asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");      // waited for before the CTAs' sums are exchanged
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, gid = lane >> 2, tig = lane & 3;
   const uint32_t CL = gridDim.x, rank = blockIdx.x;     // the cluster is the grid's row
   const int oct = blockIdx.y % n_oct, bh = blockIdx.y / n_oct, b = bh / Hkv, h = bh % Hkv;
   const int g0 = oct * 8, GV = G - g0 < 8 ? G - g0 : 8;
   const int64_t row0 = int64_t(b) * Hq + int64_t(h) * G + g0;
   uint8_t* stage = qsm + warp * A::STAGE;
-  float* cta_part = reinterpret_cast<float*>(qsm + kQdWarps * A::STAGE);
-  float* scs = reinterpret_cast<float*>(qsm + kQdWarps * A::STAGE + A::MERGE);     // [GV][K], x log2 e
+  float* inbox = reinterpret_cast<float*>(qsm + kQdWarps * A::STAGE);
+  float* scs = reinterpret_cast<float*>(qsm + kQdWarps * A::STAGE + A::INBOX * 4);     // [GV][K], x log2 e
   uint8_t* spot = reinterpret_cast<uint8_t*>(scs + A::LISTS);                       // [pair][8 heads]: slot, 0xFF: not kept
-  int32_t* ids = reinterpret_cast<int32_t*>(spot + A::LISTS * 8);                   // [GV][K]
-  int32_t* pages = ids + A::LISTS;
-  int2* items = reinterpret_cast<int2*>(pages + A::LISTS);                            // (page, pair; -1 - w: window chunk w)
-  __shared__ int s_count[kQdWarps];
+  uint32_t* ids = reinterpret_cast<uint32_t*>(spot + A::LISTS * 8);                 // [GV][K]
+  int2* items = reinterpret_cast<int2*>(ids + A::LISTS);                            // (page, pair; -1 - w: window chunk w)
+  __shared__ int s_count[kQdWarps + 1];
   const uint32_t stage_a = uint32_t(__cvta_generic_to_shared(stage));
 
   // queries as the column operand: head gid, dims 32 g + 8 tig + {i, i + 4} in
@@ -400,7 +403,7 @@ quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, co
   const int64_t n_cand = own - wm1 > 0 ? own - wm1 : 0;
   const int n_sel = own < 0 ? 0 : GV * K;
   const int n_win = own < 0 ? 0 : int(own < wm1 ? own + 1 : wm1 + 1);
-  constexpr int TH = kQdWarps * 32;
+  constexpr int TH = kQdWarps * 32, PER = A::LISTS / TH;      // kept pairs per thread, at most
   // the window's pages do not depend on the selection
   int win_page = -1;
   if (tid < n_win) {
@@ -411,59 +414,76 @@ quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, co
     }
   }
   pdl_wait();      // the top-K lists
-  for (int i = tid; i < n_sel; i += TH) {
-    const int4 k = __ldg(reinterpret_cast<const int4*>(kept + row0 * K + i));
-    ids[i] = k.x;
-    pages[i] = k.y;
-    scs[i] = __int_as_float(k.z) * kLog2e;
-  }
-  for (int i = tid; i < n_sel * 2; i += TH) reinterpret_cast<uint32_t*>(spot)[i] = 0xFFFFFFFFu;
-  __syncthreads();
-  // who else kept the chunk of each (head, slot) pair: one lane per (pair,
-  // head), binary search in the head's ascending list (-1 padding behind).  The
-  // first head that kept a chunk owns it: its pair becomes an item
-  {
-    const int GP = GV <= 1 ? 1 : GV <= 2 ? 2 : GV <= 4 ? 4 : 8;
-    const int base = lane & ~(GP - 1), g = lane & (GP - 1);
-    for (int p0 = warp * 32; p0 < n_sel * GP; p0 += TH) {
-      const int pair = (p0 + lane) / GP;
-      const int c = pair < n_sel ? ids[pair] : -1;
-      int at = -1;
-      if (c >= 0 && c < n_cand && g < GV) {
-        const int32_t* list = ids + g * K;
-        int lo = 0, hi = K - 1;
-        while (lo <= hi) {
-          const int mid = (lo + hi) >> 1, v = list[mid];
-          if (v == c) { at = mid; break; }
-          if (v >= 0 && v < c) lo = mid + 1; else hi = mid - 1;
-        }
-      }
-      const uint32_t kept = __ballot_sync(0xffffffffu, at >= 0) >> base;
-      if (at >= 0) {
-        const bool owner = (kept & ((1u << (pair / K)) - 1u)) == 0u;
-        if (owner) spot[pair * 8 + g] = uint8_t(at);
-      } else if (c >= n_cand && g == 0) {
-        record_error(HILS_ERR_DEVICE_BOUNDS);
-      }
+  int4 mine[PER];
+#pragma unroll
+  for (int e = 0; e < PER; ++e) {
+    const int pair = tid + e * TH;
+    mine[e] = make_int4(-1, -1, 0, 0);
+    if (pair < n_sel) {
+      mine[e] = __ldg(reinterpret_cast<const int4*>(kept + row0 * K + pair));
+      ids[pair] = uint32_t(mine[e].x);
+      scs[pair] = __int_as_float(mine[e].z) * kLog2e;
     }
   }
   __syncthreads();
-  // the items: the window's chunks, then the pairs that own their chunk
+  // Who else kept the chunk of each (head, slot) pair: a thread per pair, a
+  // binary search in every head's ascending list (as unsigned numbers the -1
+  // behind the ids is the largest), four heads' searches interleaved.  The first
+  // head that kept a chunk owns it: its pair becomes an item.  The window's
+  // chunks are the first items.
   int n_items = 0;
-  for (int p0 = 0; p0 < n_sel + n_win; p0 += TH) {
-    // the window's chunks first (their items are found without the selection)
-    const int pair = p0 + tid - n_win;
-    const int page = pair < 0 ? win_page : pair < n_sel && spot[pair * 8 + pair / K] != 0xFF ? pages[pair] : -1;
-    const uint32_t have = __ballot_sync(0xffffffffu, page >= 0);
+  if (n_win > 0) {
+    if (warp == 0) {
+      const uint32_t have = __ballot_sync(0xffffffffu, win_page >= 0);
+      if (win_page >= 0) items[__popc(have & ((1u << lane) - 1u))] = make_int2(win_page, -1 - tid);
+      if (lane == 0) s_count[kQdWarps] = __popc(have);
+    }
+  } else if (tid == 0) {
+    s_count[kQdWarps] = 0;
+  }
+#pragma unroll
+  for (int e = 0; e < PER; ++e) {
+    if (e * TH >= n_sel && e > 0) break;      // the same for the whole CTA
+    const int pair = tid + e * TH;
+    const uint32_t c = uint32_t(mine[e].x);
+    bool owner = false;
+    if (pair < n_sel && mine[e].x >= 0) {
+      const int g_own = pair / K;
+      uint32_t place[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
+      owner = int64_t(mine[e].x) < n_cand;
+      if (!owner) record_error(HILS_ERR_DEVICE_BOUNDS);
+#pragma unroll 1
+      for (int q = 0; q < GV; q += 4) {
+        const uint32_t* list = ids + q * K;
+        int at[4] = {0, 0, 0, 0};
+#pragma unroll 1
+        for (int st = kMaxTopK; st > 0; st >>= 1)
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+            if (q + g < GV && at[g] + st <= K && list[g * K + at[g] + st - 1] < c) at[g] += st;
+        uint32_t four = 0xFFFFFFFFu;
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          if (q + g < GV && at[g] < K && list[g * K + at[g]] == c) {
+            four ^= uint32_t(0xFF ^ at[g]) << (8 * g);
+            if (q + g < g_own) owner = false;
+          }
+        if (q == 0) place[0] = four; else place[1] = four;
+      }
+      if (owner) *reinterpret_cast<uint2*>(spot + pair * 8) = make_uint2(place[0], place[1]);
+    }
+    const bool item = owner && mine[e].y >= 0;
+    const uint32_t have = __ballot_sync(0xffffffffu, item);
     if (lane == 0) s_count[warp] = __popc(have);
     __syncthreads();
-    int at = n_items + __popc(have & ((1u << lane) - 1u));
+    if (e == 0) n_items = s_count[kQdWarps];
+    int to = n_items + __popc(have & ((1u << lane) - 1u));
 #pragma unroll
     for (int w = 0; w < kQdWarps; ++w) {
-      if (w < warp) at += s_count[w];
+      if (w < warp) to += s_count[w];
       n_items += s_count[w];
     }
-    if (page >= 0) items[at] = make_int2(page, pair >= 0 ? pair : -1 - tid);
+    if (item) items[to] = make_int2(mine[e].y, pair);
     __syncthreads();
   }
 
@@ -495,10 +515,22 @@ quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, co
     w.u[1] = __shfl_sync(0xffffffffu, mine, 2 * tig + 1);
     return w;
   };
+  // the staged rows of 64 bytes of codes have the 16-byte pieces of rows 2, 3
+  // (mod 4) swapped in halves: with the order of keys below, the 8-byte reads
+  // of four rows then fall in different banks
   auto copy = [&](const uint8_t* src, uint32_t dst) {
 #pragma unroll
-    for (int i = 0; i < A::BLOCK / 512; ++i) cp_async16(dst + uint32_t(lane + 32 * i) * 16u, src + (lane + 32 * i) * 16);
+    for (int i = 0; i < A::BLOCK / 512; ++i) {
+      const int at = lane + 32 * i;
+      const int to = D == 128 && i < kChunk * P::ROW / 512 ? at ^ ((at >> 2) & 2) : at;
+      cp_async16(dst + uint32_t(to) * 16u, src + at * 16);
+    }
   };
+  // keys as rows of the products: row r of eight is key r / 2 (r even) or
+  // 4 + (r / 2 ^ 1) (r odd), so that the rows 2 tig + j of the four tig, and the
+  // rows 2 i, 2 i + 1, lie in different banks
+  const int key_row = gid & 1 ? 4 + ((gid >> 1) ^ 1) : gid >> 1;      // of row gid
+  const int key_even = tig, key_odd = 4 + (tig ^ 1);                  // of rows 2 tig, 2 tig + 1
   auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
   auto wait_all_but_one = [] { asm volatile("cp.async.wait_group 1;" ::: "memory"); };
 
@@ -517,7 +549,7 @@ quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, co
     const Work nxt = find(item);
     wait_all_but_one();
     __syncwarp();
-    // ---- logits: tile t, rows are keys 16 t + gid and + 8, columns heads 2 tig, 2 tig + 1
+    // ---- logits: tile t of 16 keys, rows gid and gid + 8, columns heads 2 tig, 2 tig + 1
     float z[4][4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
@@ -526,10 +558,10 @@ quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, co
       uint32_t la[2];          // NS == 1: least values of groups 2 tig, 2 tig + 1
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const int key = 16 * t + 8 * r + gid;
+        const int key = 16 * t + 8 * r + key_row;
         const uint8_t* par = stage + P::param_off(key);
         if constexpr (NG == 4) {
-          const uint4 u = *reinterpret_cast<const uint4*>(stage + P::code_off(key) + 16 * tig);
+          const uint4 u = *reinterpret_cast<const uint4*>(stage + P::code_off(key) + 16 * (tig ^ (key & 2)));
           cu[r][0] = u.x; cu[r][1] = u.y; cu[r][2] = u.z; cu[r][3] = u.w;
         } else {
           const uint2 u = *reinterpret_cast<const uint2*>(stage + P::code_off(key) + 8 * tig);
@@ -539,20 +571,28 @@ quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, co
           const uint2 m = *reinterpret_cast<const uint2*>(par + 8 * (tig % (NG / 2)));
           la[r] = tig < NG / 2 ? __byte_perm(m.x, m.y, 0x7632) : 0u;
         }
+        uint32_t pw[NG];
+        if constexpr (NG == 4) {
+          const uint4 u = *reinterpret_cast<const uint4*>(par);
+          pw[0] = u.x; pw[1] = u.y; pw[2] = u.z; pw[3] = u.w;
+        } else {
+          const uint2 u = *reinterpret_cast<const uint2*>(par);
+          pw[0] = u.x; pw[1] = u.y;
+        }
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-          const float2 sm = __half22float2(reinterpret_cast<const __half2*>(par)[g]);
+          const float2 sm = __half22float2(*reinterpret_cast<const __half2*>(&pw[g]));
           ps[r][g] = sm.x;
           pm[r][g] = sm.y;
         }
       }
-      z[t][0] = z[t][1] = z[t][2] = z[t][3] = 0.f;
       // sum_g m_g sum_{i in g} q_i: fp32 models below, else one instruction,
       // the sums of q split into two fp16 (22 bits)
-      if constexpr (NS == 1) mma16816_f16(z[t], la[0], la[1], la[0], la[1], qs2[0], qs2[1]);
+      if constexpr (NS == 1) mma16816_f16_first(z[t], la[0], la[1], la[0], la[1], qs2[0], qs2[1]);
+      else z[t][0] = z[t][1] = z[t][2] = z[t][3] = 0.f;
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
-        float c[4] = {0.f, 0.f, 0.f, 0.f};
+        float c[4];
         uint32_t a[2][4];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
@@ -560,12 +600,13 @@ quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, co
           else codes_bf16<true>(__byte_perm(cu[r][g / 2], cu[r][NG / 2 + g / 2], g & 1 ? 0x7632 : 0x5410), a[r]);
         }
         if constexpr (NS == 1) {
-          mma16816_f16(c, a[0][0], a[1][0], a[0][1], a[1][1], qb[0][g][0], qb[0][g][1]);
+          mma16816_f16_first(c, a[0][0], a[1][0], a[0][1], a[1][1], qb[0][g][0], qb[0][g][1]);
           mma16816_f16(c, a[0][2], a[1][2], a[0][3], a[1][3], qb[0][g][2], qb[0][g][3]);
         } else {
 #pragma unroll
           for (int n = NS - 1; n >= 0; --n) {
-            mma16816_bf16(c, a[0][0], a[1][0], a[0][1], a[1][1], qb[n][g][0], qb[n][g][1]);
+            if (n == NS - 1) mma16816_bf16_first(c, a[0][0], a[1][0], a[0][1], a[1][1], qb[n][g][0], qb[n][g][1]);
+            else mma16816_bf16(c, a[0][0], a[1][0], a[0][1], a[1][1], qb[n][g][0], qb[n][g][1]);
             mma16816_bf16(c, a[0][2], a[1][2], a[0][3], a[1][3], qb[n][g][2], qb[n][g][3]);
           }
         }
@@ -585,7 +626,7 @@ quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, co
       for (int t = 0; t < 4; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (16 * t + 8 * (i / 2) + gid >= cur.keys) z[t][i] = -INFINITY;
+          if (16 * t + 8 * (i / 2) + key_row >= cur.keys) z[t][i] = -INFINITY;
     }
     __syncwarp();
     if (nxt.block >= 0) copy(kpg + nxt.block, stage_a);
@@ -628,18 +669,24 @@ quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, co
     __syncwarp();
     // ---- output
     const uint8_t* vst = stage + A::BLOCK;
+    if (cur.keys < kChunk) {      // the own chunk: parameters behind the sequence may be anything, their weights are 0
+      for (int key = cur.keys + lane; key < kChunk; key += 32)
+#pragma unroll
+        for (int g = 0; g < NG; ++g) *reinterpret_cast<uint32_t*>(stage + A::BLOCK + P::param_off(key) + 4 * g) = 0u;
+      __syncwarp();
+    }
     float lm[4] = {0.f, 0.f, 0.f, 0.f};      // the chunk's least values, one row per group
     const uint32_t kept_mask = (cur.heads >> gid) & 1u ? 0xFFFFFFFFu : 0u;   // of the column this lane feeds
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      // the weights with heads as columns: keys 16 t + 2 tig + {0, 1} and + 8 of head gid
+      // the weights with heads as columns: keys of rows 2 tig, 2 tig + 1 and + 8, head gid
       uint32_t wb[2];        // fp16 pairs
       float wf[2][2];        // or fp32
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const float w0 = z[t][2 * r] * coef[0], w1 = z[t][2 * r + 1] * coef[1];
         if constexpr (NS == 1) {
-          wb[r] = movmatrix(pack_f16(w0, w1)) & kept_mask;
+          wb[r] = movmatrix(pack_f16(w0, w1));
         } else {
           const uint32_t lo = movmatrix(__byte_perm(__float_as_uint(w0), __float_as_uint(w1), 0x5410)) & kept_mask;
           const uint32_t hi = movmatrix(__byte_perm(__float_as_uint(w0), __float_as_uint(w1), 0x7632)) & kept_mask;
@@ -647,15 +694,15 @@ quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, co
           wf[r][1] = __uint_as_float(__byte_perm(lo, hi, 0x7632));
         }
       }
-      uint32_t vc[2][2][NG / 2], vp[2][2][NG];    // codes and parameters of key 16 t + 8 r + 2 tig + j
+      uint32_t vc[2][2][NG / 2], vp[2][2][NG];    // codes and parameters of the key of row 8 r + 2 tig + j
       uint32_t vl[2][2];                          // parameters of group gid
 #pragma unroll
       for (int r = 0; r < 2; ++r)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const int key = 16 * t + 8 * r + 2 * tig + j;
+          const int key = 16 * t + 8 * r + (j ? key_odd : key_even);
           if constexpr (NG == 4) {
-            const uint2 u = *reinterpret_cast<const uint2*>(vst + P::code_off(key) + 8 * gid);
+            const uint2 u = *reinterpret_cast<const uint2*>(vst + P::code_off(key) + 8 * (gid ^ (2 * (key & 2))));
             vc[r][j][0] = u.x;
             vc[r][j][1] = u.y;
             const uint4 p = *reinterpret_cast<const uint4*>(vst + P::param_off(key));
@@ -670,11 +717,6 @@ quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, co
             vp[r][j][1] = p.y;
           }
           if constexpr (NS == 1) vl[r][j] = gid < NG ? *reinterpret_cast<const uint32_t*>(vst + P::param_off(key) + 4 * gid) : 0u;
-          if (cur.keys < kChunk && key >= cur.keys) {     // behind the sequence they may be anything
-#pragma unroll
-            for (int g = 0; g < NG; ++g) vp[r][j][g] = 0u;
-            vl[r][j] = 0u;
-          }
         }
       // least values of group gid as the rows of one product with the weights
       if constexpr (NS == 1)
@@ -744,7 +786,7 @@ quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, co
   __syncwarp();
 
   // ---- the warp's sums to its stage: row per head, then (maximum, sum)
-  float* mine = reinterpret_cast<float*>(stage);
+  float* sums = reinterpret_cast<float*>(stage);
 #pragma unroll
   for (int g = 0; g < NG; ++g)
 #pragma unroll
@@ -756,53 +798,55 @@ quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, co
         f4 = 1048576.f;
       }
       // dims 32 g + 4 gid + 0 .. 3
-      *reinterpret_cast<float4*>(mine + (2 * tig + e) * A::RS + 32 * g + 4 * gid) =
+      *reinterpret_cast<float4*>(sums + (2 * tig + e) * A::RS + 32 * g + 4 * gid) =
           make_float4(fmaf(acc[g][0][e], f, add), fmaf(acc[g][0][2 + e], f4, add), fmaf(acc[g][1][e], f, add),
                       fmaf(acc[g][1][2 + e], f4, add));
     }
   if (gid == 0)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      mine[8 * A::RS + 2 * (2 * tig + e)] = M[e];
-      mine[8 * A::RS + 2 * (2 * tig + e) + 1] = Z[e];
+      sums[8 * A::RS + 2 * (2 * tig + e)] = M[e];
+      sums[8 * A::RS + 2 * (2 * tig + e) + 1] = Z[e];
     }
   __syncthreads();
-  // ---- warps to the CTA's sums
+  // ---- warps to the CTA's sums, straight to the CTA that finishes the head:
+  // CTA g % CL of the cluster, which keeps a row per CTA for each of its heads
   constexpr int WS = A::STAGE / 4;
   const float* all = reinterpret_cast<const float*>(qsm);
-  for (int i = tid; i < GV * D; i += kQdWarps * 32) {
+  cg::cluster_group cluster = cg::this_cluster();
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");      // every CTA has started
+  for (int i = tid; i < GV * D; i += TH) {
     const int g = i / D, t = i % D;
-    float m = -INFINITY, s = 0.f, zz = 0.f;
-#pragma unroll
-    for (int w = 0; w < kQdWarps; ++w) m = fmaxf(m, all[w * WS + 8 * A::RS + 2 * g]);
+    float mw[kQdWarps], m = -INFINITY, s = 0.f, zz = 0.f;
 #pragma unroll
     for (int w = 0; w < kQdWarps; ++w) {
-      const float mw = all[w * WS + 8 * A::RS + 2 * g];
-      if (mw == -INFINITY) continue;       // attended nothing for this head
-      const float f = exp2f(mw - m);
+      mw[w] = all[w * WS + 8 * A::RS + 2 * g];
+      m = fmaxf(m, mw[w]);
+    }
+#pragma unroll
+    for (int w = 0; w < kQdWarps; ++w) {
+      if (mw[w] == -INFINITY) continue;       // attended nothing for this head
+      const float f = exp2f(mw[w] - m);
       s = fmaf(f, all[w * WS + g * A::RS + t], s);
       zz = fmaf(f, all[w * WS + 8 * A::RS + 2 * g + 1], zz);
     }
-    cta_part[g * A::RS + t] = s;
-    if (t == 0) {
-      cta_part[8 * A::RS + 2 * g] = m;
-      cta_part[8 * A::RS + 2 * g + 1] = zz;
-    }
+    const uint32_t turn = uint32_t(g) / CL, to = uint32_t(g) - turn * CL;
+    float* row = cluster.map_shared_rank(inbox, to) + (turn * CL + rank) * A::PART;
+    row[t] = s;
+    if (t < 2) row[D + t] = t ? zz : m;
   }
-  // ---- CTAs to the output: CTA `rank` finishes heads rank, rank + CL, ...
-  cg::cluster_group cluster = cg::this_cluster();
   cluster.sync();
-  for (int g = int(rank); g < GV; g += int(CL)) {
-    for (int t = tid; t < D; t += kQdWarps * 32) {
+  for (uint32_t g = rank, turn = 0; g < uint32_t(GV); g += CL, ++turn) {
+    for (int t = tid; t < D; t += TH) {
+      const float* rows = inbox + turn * CL * A::PART;
       float m = -INFINITY, s = 0.f, zz = 0.f;
-      for (uint32_t c = 0; c < CL; ++c) m = fmaxf(m, cluster.map_shared_rank(cta_part, c)[8 * A::RS + 2 * g]);
+      for (uint32_t c = 0; c < CL; ++c) m = fmaxf(m, rows[c * A::PART + D]);
       for (uint32_t c = 0; c < CL; ++c) {
-        const float* part = cluster.map_shared_rank(cta_part, c);
-        const float mc = part[8 * A::RS + 2 * g];
+        const float mc = rows[c * A::PART + D];
         if (mc == -INFINITY) continue;
         const float f = exp2f(mc - m);
-        s = fmaf(f, part[g * A::RS + t], s);
-        zz = fmaf(f, part[8 * A::RS + 2 * g + 1], zz);
+        s = fmaf(f, rows[c * A::PART + t], s);
+        zz = fmaf(f, rows[c * A::PART + D + 1], zz);
       }
       const float y = zz != 0.f ? s / zz : 0.f;       // nothing attended: 0
       T* out = o + (row0 + g) * D + t;
@@ -810,7 +854,6 @@ quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, co
       else *out = y;
     }
   }
-  cluster.sync();      // no CTA leaves while its sums are read
 }
 
 }  // namespace hils
