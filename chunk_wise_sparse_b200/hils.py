@@ -713,9 +713,9 @@ def landmark_summary_append(k_pages, page_table, lq, seqlens, n_tokens, summ: Su
 
 
 def decode_step_quant(q, k_pages, v_pages, page_table, summ: Summary, seqlens, topk, q_score=None, workspace=None,
-                      stream=None, window=0, out=None):
+                      stream=None, window=0, out=None, with_selection=False):
     """One decode step for q [B,Hq,d] against a 4-bit chunk-paged cache; q_score: a separate scoring query (Q-Cal).
-    Returns (o, ids, scores)."""
+    Returns (o, ids, scores); ids and scores [B,Hq,topk] only with_selection, else None."""
     dtype = q.dtype
     quant, n_pages, Hkv, d = _page_kind(k_pages, v_pages, dtype)
     if not quant:
@@ -733,8 +733,10 @@ def decode_step_quant(q, k_pages, v_pages, page_table, summ: Summary, seqlens, t
         out = _new(q, (B, Hq, d), dtype, stream)
     else:
         _need(out, "out", dtype, (B, Hq, d))
-    ids = _new(q, (B, Hq, topk), torch.int32, stream)
-    scores = _new(q, (B, Hq, topk), torch.float32, stream)
+    ids = scores = None
+    if with_selection:
+        ids = _new(q, (B, Hq, topk), torch.int32, stream)
+        scores = _new(q, (B, Hq, topk), torch.float32, stream)
     hils_attn_decode_quant(_dims_of(*key), q, q_score, k_pages, v_pages, page_table, n_pages, summ.kprime, summ.bprime,
                            summ.kprime_mma, seqlens, out, ids, scores, workspace, workspace.nbytes, stream)
     return out, ids, scores

@@ -76,7 +76,7 @@ def _against_oracle(m, lens, K, window, got, q_score=None):
 def test_decode_matches_the_oracle(dtype, B, Hq, Hkv, d, cap, K, window, lens):
     m = _cache(B, Hq, Hkv, d, cap, dtype, seed=Hq + d)
     seq = torch.tensor(lens, dtype=torch.int32, device="cuda")
-    got = hils.decode_step_quant(m["q"], m["kp"], m["vp"], m["table"], m["summ"], seq, K, window=window)
+    got = hils.decode_step_quant(m["q"], m["kp"], m["vp"], m["table"], m["summ"], seq, K, window=window, with_selection=True)
     assert hils.hils_get_status() == 0
     _against_oracle(m, np.array(lens), K, window, got)
 
@@ -86,7 +86,7 @@ def test_decode_more_candidates_than_registers_hold():
     m = _cache(1, 2, 1, 64, 64 * 9000, "bf16", seed=5)
     lens = np.array([64 * 9000 - 17])
     got = hils.decode_step_quant(m["q"], m["kp"], m["vp"], m["table"], m["summ"],
-                                 torch.from_numpy(lens.astype(np.int32)).cuda(), 32)
+                                 torch.from_numpy(lens.astype(np.int32)).cuda(), 32, with_selection=True)
     assert hils.hils_get_status() == 0
     _against_oracle(m, lens, 32, 0, got)
 
@@ -104,7 +104,7 @@ def test_decode_equals_the_unquantised_step_on_the_values_read_back(dtype):
     assert np.array_equal(kc.float().cpu().numpy(), torch.from_numpy(m["k"]).to(dt).float().numpy())
     assert np.array_equal(vc.float().cpu().numpy(), torch.from_numpy(m["v"]).to(dt).float().numpy())
     seq = torch.tensor([cap, 1500], dtype=torch.int32, device="cuda")
-    o, ids, sc = hils.decode_step_quant(m["q"], m["kp"], m["vp"], m["table"], m["summ"], seq, 16)
+    o, ids, sc = hils.decode_step_quant(m["q"], m["kp"], m["vp"], m["table"], m["summ"], seq, 16, with_selection=True)
     o2, ids2, sc2 = hils.decode_step(m["q"], kc, vc, m["summ"], seq, 16)
     assert hils.hils_get_status() == 0
     assert torch.equal(ids, ids2) and (sc - sc2).abs().max().item() <= 1e-5
@@ -116,7 +116,7 @@ def test_decode_with_a_scoring_query_and_without_optional_outputs():
     lens = np.array([2048, 1300])
     seq = torch.from_numpy(lens.astype(np.int32)).cuda()
     qs = torch.randn((2, 8, 64), device="cuda").bfloat16()
-    got = hils.decode_step_quant(m["q"], m["kp"], m["vp"], m["table"], m["summ"], seq, 8, q_score=qs)
+    got = hils.decode_step_quant(m["q"], m["kp"], m["vp"], m["table"], m["summ"], seq, 8, q_score=qs, with_selection=True)
     assert hils.hils_get_status() == 0
     _against_oracle(m, lens, 8, 0, got, q_score=qs)
     dims = hils.make_dims(2, 8, 2, 64, 2048, 8, torch.bfloat16)
@@ -125,6 +125,8 @@ def test_decode_with_a_scoring_query_and_without_optional_outputs():
     hils.hils_attn_decode_quant(dims, m["q"], qs, m["kp"], m["vp"], m["table"], m["n_pages"], None, None,
                                 m["summ"].kprime_mma, seq, o, None, None, ws)
     assert torch.equal(o, got[0])
+    o2, ids, sc = hils.decode_step_quant(m["q"], m["kp"], m["vp"], m["table"], m["summ"], seq, 8, q_score=qs)
+    assert torch.equal(o2, o) and ids is None and sc is None
 
 
 def test_rows_behind_the_sequence_are_not_looked_at():
@@ -155,10 +157,10 @@ def test_rows_behind_the_sequence_are_not_looked_at():
 def test_decode_records_bad_pages_and_lengths():
     m = _cache(3, 4, 2, 64, 1024, "bf16", seed=11)
     seq = torch.tensor([1024, 1000, 900], dtype=torch.int32, device="cuda")
-    want, ids, _ = hils.decode_step_quant(m["q"], m["kp"], m["vp"], m["table"], m["summ"], seq, 4)
+    want, ids, _ = hils.decode_step_quant(m["q"], m["kp"], m["vp"], m["table"], m["summ"], seq, 4, with_selection=True)
     bad = m["table"].clone()
     bad[1, int(ids[1, 0, 0])] = m["n_pages"]
-    o, ids2, _ = hils.decode_step_quant(m["q"], m["kp"], m["vp"], bad, m["summ"], seq, 4)
+    o, ids2, _ = hils.decode_step_quant(m["q"], m["kp"], m["vp"], bad, m["summ"], seq, 4, with_selection=True)
     assert hils.hils_get_status() == 6
     assert torch.equal(ids, ids2) and torch.equal(o[[0, 2]], want[[0, 2]]) and bool(torch.isfinite(o.float()).all())
     assert not torch.equal(o[1, 0], want[1, 0])
@@ -168,7 +170,8 @@ def test_decode_records_bad_pages_and_lengths():
     assert hils.hils_get_status() == 6 and bool((o == 0).all())
     for n in (0, -1, 1025):
         seq2 = torch.tensor([1024, n, 900], dtype=torch.int32, device="cuda")
-        o, ids2, sc = hils.decode_step_quant(m["q"], m["kp"], m["vp"], m["table"], m["summ"], seq2, 4)
+        o, ids2, sc = hils.decode_step_quant(m["q"], m["kp"], m["vp"], m["table"], m["summ"], seq2, 4,
+                                             with_selection=True)
         assert hils.hils_get_status() == 6
         assert torch.equal(o[[0, 2]], want[[0, 2]]) and bool((o[1] == 0).all()) and bool((ids2[1] == -1).all())
         assert bool((sc[1] == float("-inf")).all())
@@ -180,7 +183,7 @@ def test_large_logits_and_equal_rows():
     m["q"].mul_(20)
     lens = np.array([1024])
     seq = torch.tensor([1024], dtype=torch.int32, device="cuda")
-    o, ids, _ = hils.decode_step_quant(m["q"], m["kp"], m["vp"], m["table"], m["summ"], seq, 4, window=128)
+    o, ids, _ = hils.decode_step_quant(m["q"], m["kp"], m["vp"], m["table"], m["summ"], seq, 4, window=128, with_selection=True)
     assert hils.hils_get_status() == 0
     oracle = Oracle(1, 4, 2, 1024, 64, C, 4, 128)
     kp, bp = oracle.summary(m["k"], m["lq"].cpu().numpy())
@@ -193,8 +196,31 @@ def test_large_logits_and_equal_rows():
     same = torch.zeros_like(m["table"])
     m["summ"].kprime[:] = m["summ"].kprime[:, :, :1].clone()
     m["summ"].bprime[:] = m["summ"].bprime[:, :, :1].clone()
-    _, ids, _ = hils.decode_step_quant(m["q"], m["kp"], m["vp"], same, m["summ"], seq, 4)
+    _, ids, _ = hils.decode_step_quant(m["q"], m["kp"], m["vp"], same, m["summ"], seq, 4, with_selection=True)
     assert ids.view(4, 4).tolist() == [[0, 1, 2, 3]] * 4
+
+
+@pytest.mark.parametrize("cap", [64 * 700, 64 * 3000, 64 * 33000])
+def test_tied_scores_go_to_the_lower_ids(cap):
+    """More equal scores than a row's threads: the K kept ones are those above the tie and then the lowest ids of it
+    (the row in registers of 256 or 1024 threads, and beyond what registers hold)."""
+    K, nc = 16, cap // C
+    kp, vp = hils.quant_pages(1, 1, 64), hils.quant_pages(1, 1, 64)
+    table = torch.zeros((1, nc), dtype=torch.int32, device="cuda")      # every chunk is the one page
+    q = torch.ones((1, 2, 64), device="cuda")
+    bias = torch.zeros((1, 1, nc), device="cuda")
+    above = [5, 300, 301, nc - 2]
+    bias[0, 0, above] = 1.0
+    bias[0, 0, 7:20] = -1.0
+    bias[0, 0, 2] = float("-inf")
+    summ = hils.Summary.of(torch.zeros((1, 1, nc, 64), device="cuda"), bias)
+    seq = torch.tensor([cap], dtype=torch.int32, device="cuda")
+    _, ids, sc = hils.decode_step_quant(q, kp, vp, table, summ, seq, K, with_selection=True)
+    assert hils.hils_get_status() == 0
+    tied = [c for c in range(nc - 1) if c not in above and not 7 <= c < 20 and c != 2]
+    want = sorted(above + tied[: K - len(above)])
+    assert ids.view(2, K).tolist() == [want] * 2
+    assert sc.view(2, K).tolist() == [[1.0 if c in above else 0.0 for c in want]] * 2
 
 
 class _Loop:
@@ -367,7 +393,7 @@ def test_two_loops_on_two_streams():
 def test_step_is_reproducible():
     m = _cache(4, 16, 4, 128, 4096, "bf16", seed=50)
     seq = torch.tensor([4096, 4000, 100, 2049], dtype=torch.int32, device="cuda")
-    first = hils.decode_step_quant(m["q"], m["kp"], m["vp"], m["table"], m["summ"], seq, 16, window=128)
+    first = hils.decode_step_quant(m["q"], m["kp"], m["vp"], m["table"], m["summ"], seq, 16, window=128, with_selection=True)
     for _ in range(5):
-        again = hils.decode_step_quant(m["q"], m["kp"], m["vp"], m["table"], m["summ"], seq, 16, window=128)
+        again = hils.decode_step_quant(m["q"], m["kp"], m["vp"], m["table"], m["summ"], seq, 16, window=128, with_selection=True)
         assert all(torch.equal(a, b) for a, b in zip(first, again))
