@@ -54,13 +54,14 @@ __device__ __forceinline__ void quant_store_row(const float (&x)[E], int sub, ui
   using P = QuantPage<D>;
   constexpr int GL = kQGroup / E;      // lanes per group
   static_assert(E == 4 || E == 8, "a lane holds one 16-byte vector of fp32 or bf16");
-  float lo = x[0], hi = x[0];
+  float lo = x[0], hi = x[0], bad = 0.f;
 #pragma unroll
   for (int e = 0; e < E; ++e) {
     lo = fminf(lo, x[e]);
     hi = fmaxf(hi, x[e]);
-    if (!(fabsf(x[e]) < INFINITY)) hi = INFINITY;   // fminf / fmaxf drop a NaN
+    bad = fmaf(x[e], 0.f, bad);       // NaN once a value is not finite (fminf and fmaxf drop a NaN)
   }
+  if (bad != 0.f) hi = INFINITY;      // true for NaN
 #pragma unroll
   for (int o = 1; o < GL; o <<= 1) {
     lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
@@ -74,21 +75,25 @@ __device__ __forceinline__ void quant_store_row(const float (&x)[E], int sub, ui
     m = 0.f;
   }
   const float inv = s > 0.f ? 1.f / s : 0.f;
+  // The quotient rounded to nearest by one correction of t * (1/s) (Markstein's
+  // theorem: 1/s is correctly rounded), so that a value half way between two
+  // codes, common among bf16 values, is seen as such.  A value below the
+  // rounded least one, or (with the step rounded down) above the largest, takes
+  // the nearest code; s = 0 gives 0, and so does the NaN of a group that is not
+  // finite.  Rounding to an integer by adding 1.5 x 2^23 and packing four codes
+  // in fp32 (exact below 2^16) keep to the full-rate pipes.
+  constexpr float kRound = 12582912.f;
   uint32_t u[E / 4];
 #pragma unroll
   for (int w = 0; w < E / 4; ++w) {
-    u[w] = 0;
+    float four = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      // the quotient rounded to nearest by one correction of t * (1/s)
-      // (Markstein's theorem: 1/s is correctly rounded), so that a value half
-      // way between two codes, common among bf16 values, is seen as such.
-      // A value below the rounded least one, or (with the step rounded down)
-      // above the largest, takes the nearest code
+    for (int i = 3; i >= 0; --i) {
       const float t = x[4 * w + i] - m, q0 = t * inv, q1 = fmaf(fmaf(-q0, s, t), inv, q0);
-      const float c = s > 0.f ? fminf(fmaxf(rintf(q1), 0.f), 15.f) : 0.f;
-      u[w] |= uint32_t(c) << (4 * i);
+      const float c = (fminf(fmaxf(q1, 0.f), 15.f) + kRound) - kRound;
+      four = fmaf(four, 16.f, c);
     }
+    u[w] = __float_as_uint(four + 8388608.f) & 0xFFFFu;
   }
   // a lane of an even group and its neighbour of the next group exchange a
   // unit, so that each stores one aligned 32-bit word
