@@ -849,7 +849,8 @@ static bool rows_ok(const hils_rows* r, const hils_dims* d, int64_t T, int64_t h
   if (r == nullptr || !ptr_ok(r->data)) return false;
   const int64_t per16 = d->dtype == HILS_BF16 ? 8 : 4, D = d->head_dim, ts = r->token_stride, hs = r->head_stride;
   if (ts < 0 || hs < 0 || ts % per16 != 0 || hs % per16 != 0) return false;
-  if (ts > (int64_t(1) << 40) || hs > (int64_t(1) << 40)) return false;
+  // every offset fits 62 bits
+  if (__int128(T - 1) * ts + __int128(heads - 1) * hs + D >= (__int128(1) << 62)) return false;
   if (!output) return true;
   if ((T > 1 && ts < D) || (heads > 1 && hs < D)) return false;
   return T == 1 || heads == 1 || ts >= (heads - 1) * hs + D || hs >= (T - 1) * ts + D;

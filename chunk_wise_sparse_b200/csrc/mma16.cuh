@@ -62,6 +62,16 @@ __device__ __forceinline__ float pow2(float x) {
   return y;
 }
 
+// The power of two that puts `top` (>= 0) in [2^14, 2^15), and its inverse,
+// within fp32's normal powers: values so scaled fit fp16, and lose at most
+// 2^-24 of the largest.
+__device__ __forceinline__ void power_scale(float top, float& up, float& down) {
+  int e = int(__float_as_uint(top) >> 23);
+  e = e < 30 ? 30 : e > 250 ? 250 : e;
+  up = __uint_as_float(uint32_t(268 - e) << 23);      // 2^(141 - e)
+  down = __uint_as_float(uint32_t(e - 14) << 23);     // 2^(e - 141)
+}
+
 // The four codes of a 16-bit unit of x and of one of y (the upper ones if
 // `upper`), side by side, as fp16 subnormals: code 0 in bits 0 .. 3 is
 // code 2^-24, code 1 left in bits 4 .. 7 is code 2^-20, and codes 2 and 3
@@ -72,6 +82,21 @@ __device__ __forceinline__ void codes_f16(uint32_t x, uint32_t y, bool upper, ui
   a[1] = lo & 0x00F000F0u;
   a[2] = hi & 0x000F000Fu;
   a[3] = hi & 0x00F000F0u;
+}
+
+// The same centred: code - 8 in a[0] and a[2], 16 (code - 8) in a[1] and a[3],
+// exactly (1024 + code, or 1024 + 16 code, has the code where it lies).  For
+// sums that have to be good to fp32: a sum of codes from 0 cancels against the
+// least values, and the matrix unit does not round its sums to nearest.
+__device__ __forceinline__ void codes_f16_centred(uint32_t x, uint32_t y, bool upper, uint32_t (&a)[4]) {
+  codes_f16(x, y, upper, a);
+  const __half2 off[2] = {__floats2half2_rn(-1032.f, -1032.f), __floats2half2_rn(-1152.f, -1152.f)};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t w = a[i] | 0x64006400u;
+    const __half2 v = __hadd2(*reinterpret_cast<const __half2*>(&w), off[i & 1]);
+    a[i] = *reinterpret_cast<const uint32_t*>(&v);
+  }
 }
 
 // Four codes of two 16-bit units as bf16 pairs: 16 + code has the code in

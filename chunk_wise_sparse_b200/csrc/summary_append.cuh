@@ -145,174 +145,195 @@ __global__ void __launch_bounds__(128) summary_append_kernel(SummaryParams p) {
   }
 }
 
-// d = a b + c on a pair of fp32 values
-__device__ __forceinline__ void fma_pair(float2& d, float2 a, float2 b, float2 c) {
-  asm("{\n\t.reg .b64 x, y, z, w;\n\t"
-      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
-      "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-}
-
-// Keys in 4 bits.  Four lanes per key row, eight rows per step; a lane has
-// eight dims of every group, which its two 16-bit units per group hold as
-// pairs (i, i + 4).  One pass: logits of a step, the running maximum (rescaled
-// only when a step raises it, about three times in eight steps), and the
-// weighted sum, all in fp32 on pairs of values (code - 8, exact in bf16, widened by a
-// shift).  WARPS warps share a chunk: 4 where chunks are few (a decode step: latency),
-// 1 where they fill the GPU (a prompt: fewer instructions).
-// Bound by instructions: about three per pair of codes and four for its two
-// products.  Measured on 2048 chunks x 16 heads of 64 dims (84 MB): see
-// launch_summary_append.
-constexpr int kSummaryAhead = 8;      // steps whose loads are in flight
-
+// Keys in 4 bits, by matrix products of 16 keys, of the codes where they lie
+// (codes_f16) and fp16 operands, as the decode step reads them; the columns that
+// one landmark query leaves free carry the precision of fp32.
+//   logits: columns 0 and 1 hold the query, scaled by a power of two that puts
+//     its largest value in [2^14, 2^15), as a sum of two fp16 values (22 bits;
+//     bf16 is exact in one): z_j = tau sum_g [ s_jg acc_jg + m_jg sum_{i in g} q_i ].
+//   sum of keys: with x_jg = p_j s_jg 2^k = hi + lo (k puts the largest step in
+//     [2^14, 2^15)), the pair (hi, lo) of a key is columns 0 and 1 of its row, and the
+//     transpose that makes the row a column operand is one instruction:
+//     k' l = 2^-k sum_j x_jg (code_j - 8) + sum_j p_j (m_jg + 8 s_jg).
+// Each WARPS warps share a chunk: 4 where chunks are few (a decode step:
+// latency), 1 where they fill the GPU (a prompt: fewer instructions, by which
+// it is bound).  Measured on 2048 chunks x 16 heads of 64 dims (84 MB): 53 us;
+// in fp32 on pairs of values 59 us, a lane per eight dims with an online
+// softmax per key 86 us.
 template <typename T, int D, int WARPS>
 __global__ void __launch_bounds__(128, D == 64 ? 5 : 3) summary_quant_kernel(SummaryParams p) {
   using P = QuantPage<D>;
   constexpr float kLog2e = 1.4426950408889634f;
-  constexpr int NG = P::G, STEPS = 8 / WARPS, AHEAD = STEPS < kSummaryAhead ? STEPS : kSummaryAhead;
+  constexpr int NG = P::G, TILES = 4 / WARPS;
+  constexpr bool EXACT = sizeof(T) == 2;      // one fp16 value holds a scaled bf16 one
   __shared__ Done found[kUnitMost];
   __shared__ int count;
   __shared__ __align__(16) float part[4][D];      // written in 16-byte pieces
   __shared__ float stat[4][3];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = lane >> 2, sub = lane & 3;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gid = lane >> 2, tig = lane & 3;
   const int per = WARPS == 4 ? p.Hkv : (p.Hkv + 3) / 4;      // CTAs per unit
   const int64_t h = WARPS == 4 ? blockIdx.x % per : int64_t(blockIdx.x % per) * 4 + warp;
   if (blockIdx.x == 0) check_batch(p.tb, threadIdx.x, 128);
   const int n = completed_chunks(p, blockIdx.x / per * p.unit, found, &count);
   if (h >= p.Hkv || n == 0) return;        // h: WARPS == 1 only, no barrier follows
-  const int row0 = (WARPS == 4 ? 16 * warp : 0) + row;
-  uint32_t code[AHEAD][NG], par[AHEAD][NG];
-  auto load = [&](int i, int st, int to) {
-    const uint8_t* block = p.k_pages + (found[i].page * int64_t(p.Hkv) + h) * P::BLOCK;
-    const int key = row0 + 8 * st;
-    if constexpr (NG == 4) {
-      const uint4 u = __ldg(reinterpret_cast<const uint4*>(block + P::code_off(key) + 16 * sub));
-      const uint4 w = __ldg(reinterpret_cast<const uint4*>(block + P::param_off(key)));
-      code[to][0] = u.x; code[to][1] = u.y; code[to][2] = u.z; code[to][3] = u.w;
-      par[to][0] = w.x; par[to][1] = w.y; par[to][2] = w.z; par[to][3] = w.w;
-    } else {
-      const uint2 u = __ldg(reinterpret_cast<const uint2*>(block + P::code_off(key) + 8 * sub));
-      const uint2 w = __ldg(reinterpret_cast<const uint2*>(block + P::param_off(key)));
-      code[to][0] = u.x; code[to][1] = u.y;
-      par[to][0] = w.x; par[to][1] = w.y;
-    }
-  };
-  constexpr int QV = sizeof(T) == 2 ? 1 : 2;      // 16-byte pieces of eight values
+  const int key0 = WARPS == 4 ? 16 * warp : 0;
+
+  // rows 16 t + 8 r + gid of a chunk: the lane's code words and all parameters
+  uint32_t code[TILES][2][NG], par[TILES][2][NG];
+  constexpr int QV = EXACT ? 1 : 2;        // 16-byte pieces of eight values
   uint4 lqv[NG][QV];
-  auto load_lq = [&](int i) {
-    const T* lqr = static_cast<const T*>(p.lq) + (found[i].unit + h * p.nc) * D + 8 * sub;
+  auto load = [&](int i) {
+    const uint8_t* block = p.k_pages + (found[i].page * int64_t(p.Hkv) + h) * P::BLOCK;
+    const T* lqr = static_cast<const T*>(p.lq) + (found[i].unit + h * p.nc) * D + 8 * tig;
+#pragma unroll
+    for (int t = 0; t < TILES; ++t)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int key = key0 + 16 * t + 8 * r + gid;
+        if constexpr (NG == 4) {
+          const uint4 u = __ldg(reinterpret_cast<const uint4*>(block + P::code_off(key) + 16 * tig));
+          const uint4 w = __ldg(reinterpret_cast<const uint4*>(block + P::param_off(key)));
+          code[t][r][0] = u.x; code[t][r][1] = u.y; code[t][r][2] = u.z; code[t][r][3] = u.w;
+          par[t][r][0] = w.x; par[t][r][1] = w.y; par[t][r][2] = w.z; par[t][r][3] = w.w;
+        } else {
+          const uint2 u = __ldg(reinterpret_cast<const uint2*>(block + P::code_off(key) + 8 * tig));
+          const uint2 w = __ldg(reinterpret_cast<const uint2*>(block + P::param_off(key)));
+          code[t][r][0] = u.x; code[t][r][1] = u.y;
+          par[t][r][0] = w.x; par[t][r][1] = w.y;
+        }
+      }
 #pragma unroll
     for (int g = 0; g < NG; ++g)
 #pragma unroll
       for (int e = 0; e < QV; ++e) lqv[g][e] = __ldg(reinterpret_cast<const uint4*>(lqr + 32 * g) + e);
   };
-  load_lq(0);
-#pragma unroll
-  for (int st = 0; st < AHEAD; ++st) load(0, st, st);
+  load(0);
   for (int i = 0; i < n; ++i) {
     const int64_t unit = found[i].unit + h * p.nc;
-    float2 lq[NG][4];       // dims 32 g + 8 sub + {i, i + 4}
-    float lsum[NG];
+    const uint8_t* block = p.k_pages + (found[i].page * int64_t(p.Hkv) + h) * P::BLOCK;
+    // ---- the query as a column operand, dims 32 g + 8 tig + {i, i + 4}; its groups' sums
+    uint32_t qb[NG][4];
+    float lsum[NG], unscale;
+    {
+      float x[NG][8], top = 0.f;
 #pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      float x[8];
-      if constexpr (QV == 1) {
-        Vec16<T>::unpack(lqv[g][0], x);
-      } else {
-        const uint32_t w[8] = {lqv[g][0].x, lqv[g][0].y, lqv[g][0].z, lqv[g][0].w,
-                               lqv[g][QV - 1].x, lqv[g][QV - 1].y, lqv[g][QV - 1].z, lqv[g][QV - 1].w};
+      for (int g = 0; g < NG; ++g) {
+        if constexpr (EXACT) {
+          Vec16<T>::unpack(lqv[g][0], x[g]);
+        } else {
+          const uint32_t w[8] = {lqv[g][0].x, lqv[g][0].y, lqv[g][0].z, lqv[g][0].w,
+                                 lqv[g][QV - 1].x, lqv[g][QV - 1].y, lqv[g][QV - 1].z, lqv[g][QV - 1].w};
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(w[e]);
+          for (int e = 0; e < 8; ++e) x[g][e] = __uint_as_float(w[e]);
+        }
+        lsum[g] = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          lsum[g] += x[g][e];
+          top = fmaxf(top, fabsf(x[g][e]));
+        }
+        lsum[g] += __shfl_xor_sync(0xffffffffu, lsum[g], 1);
+        lsum[g] += __shfl_xor_sync(0xffffffffu, lsum[g], 2);
       }
-      lsum[g] = 0.f;
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      float up;
+      power_scale(top, up, unscale);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        lq[g][e] = make_float2(x[e], x[e + 4]);
-        lsum[g] += x[e] + x[e + 4];
+      for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float f = e & 1 ? up * 0.0625f : up, a = x[g][e] * f, b = x[g][e + 4] * f;
+          const uint32_t hi = pack_f16(a, b);
+          qb[g][e] = gid == 0 ? hi : 0u;
+          if constexpr (!EXACT) {
+            const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+            if (gid == 1) qb[g][e] = pack_f16(a - back.x, b - back.y);
+          }
+        }
+      unscale *= 16777216.f;      // the codes are multiplied as code 2^-24
+    }
+    // ---- logits in base 2, in the lanes tig == 0.  The other lanes' columns are
+    // zero; what they compute from here on stays in them and in columns from 2 on
+    float z[TILES][2], m = -INFINITY;
+    __half2 step_top = __floats2half2_rn(0.f, 0.f);       // the largest step, in the lower half
+#pragma unroll
+    for (int t = 0; t < TILES; ++t) {
+      float acc[NG][4];
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        uint32_t a[2][4];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) codes_f16(code[t][r][g / 2], code[t][r][NG / 2 + g / 2], g & 1, a[r]);
+        mma16816_f16_first(acc[g], a[0][0], a[1][0], a[0][1], a[1][1], qb[g][0], qb[g][1]);
+        mma16816_f16(acc[g], a[0][2], a[1][2], a[0][3], a[1][3], qb[g][2], qb[g][3]);
+      }
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float sum = 0.f, low = 0.f;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          const float2 sm = __half22float2(*reinterpret_cast<const __half2*>(&par[t][r][g]));
+          sum = fmaf(sm.x, EXACT ? acc[g][2 * r] : acc[g][2 * r] + acc[g][2 * r + 1], sum);
+          low = fmaf(sm.y, lsum[g], low);
+          step_top = __hmax2(step_top, *reinterpret_cast<const __half2*>(&par[t][r][g]));
+        }
+        z[t][r] = fmaf(sum, unscale, low) * (p.tau * kLog2e);
+        m = fmaxf(m, z[t][r]);
       }
     }
-    float m = -INFINITY, l = 0.f, s = 0.f, low[NG];
-    float2 acc[NG][4];
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float x_up, x_down;       // steps are not negative, so their bits compare as they do
+    power_scale(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(__low2float(step_top)))), x_up, x_down);
+    // ---- weights, and the sum of keys
+    float l = 0.f, s = 0.f, low[NG], acc[NG][2][4];
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
       low[g] = 0.f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[g][e] = make_float2(0.f, 0.f);
+      for (int e = 0; e < 8; ++e) acc[g][e / 4][e % 4] = 0.f;
     }
 #pragma unroll
-    for (int st = 0; st < STEPS; ++st) {
-      const int at = st % AHEAD;
-      float2 x[NG][4];
-      float sg[NG], mg[NG], z = 0.f;
+    for (int t = 0; t < TILES; ++t) {
+      uint32_t xb[NG][2], vc[2][2][NG / 2];
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        uint32_t a[4];
-        codes_bf16<true>(__byte_perm(code[at][g / 2], code[at][NG / 2 + g / 2], g & 1 ? 0x7632 : 0x5410), a);
-        const float2 sm = __half22float2(*reinterpret_cast<const __half2*>(&par[at][g]));
-        sg[g] = sm.x;
-        mg[g] = fmaf(8.f, sm.x, sm.y);
-        float2 d = make_float2(0.f, 0.f);
+      for (int r = 0; r < 2; ++r) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[g][e] = make_float2(lo_bf16(a[e]), hi_bf16(a[e]));
-          fma_pair(d, lq[g][e], x[g][e], d);
+        for (int j = 0; j < 2; ++j) {
+          const int key = key0 + 16 * t + 8 * r + 2 * tig + j;
+          if constexpr (NG == 4) {
+            const uint2 u = __ldg(reinterpret_cast<const uint2*>(block + P::code_off(key) + 8 * gid));
+            vc[r][j][0] = u.x; vc[r][j][1] = u.y;
+          } else {
+            vc[r][j][0] = __ldg(reinterpret_cast<const uint32_t*>(block + P::code_off(key) + 4 * gid));
+          }
         }
-        z = fmaf(sg[g], d.x + d.y, fmaf(mg[g], lsum[g], z));
-      }
-      if (st + AHEAD < STEPS) load(i, st + AHEAD, at);
-      z += __shfl_xor_sync(0xffffffffu, z, 1);
-      z += __shfl_xor_sync(0xffffffffu, z, 2);
-      z *= p.tau * kLog2e;       // logits in base 2 from here on
-      float top = z;
-#pragma unroll
-      for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      if (top > m) {         // the same for the whole warp
-        const float f = pow2<true>(m - top);      // 0 the first time
-        l *= f;
-        s *= f;
+        const float w = pow2<true>(z[t][r] - m);
+        l += w;
+        s = fmaf(w, z[t][r], s);
+        const float ws = w * x_up;
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-          low[g] *= f;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) { acc[g][e].x *= f; acc[g][e].y *= f; }
+          const float2 sm = __half22float2(*reinterpret_cast<const __half2*>(&par[t][r][g]));
+          low[g] = fmaf(w, fmaf(8.f, sm.x, sm.y), low[g]);
+          const float x = ws * sm.x;
+          const __half hi = __float2half_rn(x);
+          const __half2 pair = __halves2half2(hi, __float2half_rn(x - __half2float(hi)));
+          xb[g][r] = movmatrix(*reinterpret_cast<const uint32_t*>(&pair));
         }
-        m = top;
       }
-      const float w = pow2<true>(z - m);
-      l += w;
-      s = fmaf(w, z, s);
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
-        const float ws = w * sg[g];
-        low[g] = fmaf(w, mg[g], low[g]);
+        uint32_t a[2][4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) fma_pair(acc[g][e], make_float2(ws, ws), x[g][e], acc[g][e]);
+        for (int r = 0; r < 2; ++r) codes_f16_centred(vc[r][0][g / 2], vc[r][1][g / 2], g & 1, a[r]);
+        mma16816_f16(acc[g][0], a[0][0], a[0][1], a[1][0], a[1][1], xb[g][0], xb[g][1]);
+        mma16816_f16(acc[g][1], a[0][2], a[0][3], a[1][2], a[1][3], xb[g][0], xb[g][1]);
       }
     }
     // the next chunk's loads are on their way while this one is summed up
-    if (i + 1 < n) {
-      load_lq(i + 1);
-#pragma unroll
-      for (int st = 0; st < AHEAD; ++st) load(i + 1, st, st);
-    }
-    // ---- sums over the eight rows: each lane ends with the NG sums from `own` on
-    float v[8 * NG];
-#pragma unroll
-    for (int g = 0; g < NG; ++g)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) { v[8 * g + e] = acc[g][e].x; v[8 * g + 4 + e] = acc[g][e].y; }
-    int own = 0;
-#pragma unroll
-    for (int bit = 16, half = 4 * NG; bit >= 4; bit >>= 1, half >>= 1) {
-      const bool up = lane & bit;
-      own += up ? half : 0;
-#pragma unroll
-      for (int e = 0; e < half; ++e) {
-        const float give = up ? v[e] : v[e + half], keep = up ? v[e + half] : v[e];
-        v[e] = keep + __shfl_xor_sync(0xffffffffu, give, bit);
-      }
-    }
+    if (i + 1 < n) load(i + 1);
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) {
       l += __shfl_xor_sync(0xffffffffu, l, o);
@@ -320,32 +341,35 @@ __global__ void __launch_bounds__(128, D == 64 ? 5 : 3) summary_quant_kernel(Sum
 #pragma unroll
       for (int g = 0; g < NG; ++g) low[g] += __shfl_xor_sync(0xffffffffu, low[g], o);
     }
-    const int g_own = own / 8, dim = 32 * g_own + 8 * sub + own % 8;      // NG neighbouring dims of one group
-    float add = low[0];
+    // lanes tig == 0: dims 32 g + 4 gid + 0 .. 3 (odd ones multiplied as 16 (code - 8))
+    float4 v[NG];
+    const float f0 = x_down, f1 = x_down * 0.0625f;
 #pragma unroll
-    for (int g = 1; g < NG; ++g) add = g_own == g ? low[g] : add;
+    for (int g = 0; g < NG; ++g)
+      v[g] = make_float4(fmaf(acc[g][0][0] + acc[g][0][1], f0, low[g]), fmaf(acc[g][0][2] + acc[g][0][3], f1, low[g]),
+                         fmaf(acc[g][1][0] + acc[g][1][1], f0, low[g]), fmaf(acc[g][1][2] + acc[g][1][3], f1, low[g]));
     if constexpr (WARPS == 1) {
-      const float inv = 1.f / l;
-#pragma unroll
-      for (int e = 0; e < NG; ++e) v[e] = (v[e] + add) * inv;
-      float* out = p.kp + unit * D + dim;
-      if constexpr (NG == 4) *reinterpret_cast<float4*>(out) = make_float4(v[0], v[1], v[2], v[3]);
-      else *reinterpret_cast<float2*>(out) = make_float2(v[0], v[1]);
-      const float bias = (m - s * inv) * (1.f / kLog2e) + logf(l);
-      if (lane == 0) p.bp[unit] = bias;
-      if (p.kmma != nullptr) {
+      if (tig == 0) {
+        const float inv = 1.f / l, bias = (m - s * inv) * (1.f / kLog2e) + logf(l);
+        float* out = p.kp + unit * D + 4 * gid;
         __nv_bfloat16* mrow = p.kmma + unit * (D + kExt);
-        if constexpr (NG == 4) *reinterpret_cast<uint2*>(mrow + dim) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
-        else *reinterpret_cast<uint32_t*>(mrow + dim) = pack_bf16(v[0], v[1]);
-        if (lane < 8) {      // b'/tau as the sum of two bf16 values (see summary_kernel), then zeros
-          const float x = bias / p.tau;
-          const float hi = __bfloat162float(__float2bfloat16_rn(x));
-          reinterpret_cast<uint32_t*>(mrow + D)[lane] = lane == 0 ? pack_bf16(hi, x - hi) : 0u;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          const float4 y = make_float4(v[g].x * inv, v[g].y * inv, v[g].z * inv, v[g].w * inv);
+          *reinterpret_cast<float4*>(out + 32 * g) = y;
+          if (p.kmma != nullptr) *reinterpret_cast<uint2*>(mrow + 32 * g + 4 * gid) = make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
+        }
+        if (gid == 0) p.bp[unit] = bias;
+        if (p.kmma != nullptr) {      // b'/tau as the sum of two bf16 values (see summary_kernel), then zeros
+          const float x = bias / p.tau, hi = __bfloat162float(__float2bfloat16_rn(x));
+          reinterpret_cast<uint32_t*>(mrow + D)[gid] = gid == 0 ? pack_bf16(hi, x - hi) : 0u;
         }
       }
     } else {
+      if (tig == 0) {
 #pragma unroll
-      for (int e = 0; e < NG; ++e) part[warp][dim + e] = v[e] + add;
+        for (int g = 0; g < NG; ++g) *reinterpret_cast<float4*>(&part[warp][32 * g + 4 * gid]) = v[g];
+      }
       if (lane == 0) { stat[warp][0] = m; stat[warp][1] = l; stat[warp][2] = s; }
       __syncthreads();
       if (threadIdx.x < D) {

@@ -629,7 +629,9 @@ def _new(like, shape, dtype, stream):
     other stream's work before they end."""
     if stream is None:
         return like.new_empty(shape, dtype=dtype)
-    with torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream):
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    with torch.cuda.stream(stream):
         return like.new_empty(shape, dtype=dtype)
 
 

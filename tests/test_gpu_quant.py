@@ -390,6 +390,57 @@ def test_two_loops_on_two_streams():
         assert torch.equal(a.o, b.o) and torch.equal(a.kp, b.kp) and torch.equal(a.summ.kprime, b.summ.kprime)
 
 
+def test_empty_calls_and_default_stream_handles():
+    """No tokens: nothing is launched, nothing changes; stream=0 is the default stream."""
+    for quant in (False, True):
+        loop = _Loop(quant)
+        before = hils.hils_kernel_launches()
+        none = loop.x[0, :0]
+        q, k, v = loop._split(none)
+        cu = torch.zeros(loop.B + 1, dtype=torch.int32, device="cuda")
+        out = hils.kv_append(loop.kp, loop.vp, loop.table, k, v, loop.seqlens, cu_tokens=cu, rotary=loop.rotary, q=q)
+        assert out.shape == (0, loop.Hq, loop.d)
+        hils.landmark_summary_append(loop.kp, loop.table, loop.lq, loop.seqlens, 0, loop.summ, cu_tokens=cu)
+        if quant:
+            k, v = hils.kv_read(loop.kp, loop.vp, loop.table, loop.seqlens, 0, torch.bfloat16)
+            assert k.shape == v.shape == (0, loop.Hkv, loop.d)
+        assert hils.hils_kernel_launches() == before and bool((loop.kp == 0).all())
+    a, b = _Loop(True, seed=60), _Loop(True, seed=60)
+    for loop, stream in ((a, None), (b, 0)):
+        loop.prompt([61, 128, 250], stream=stream)
+        loop.feed()
+        loop.step(stream=stream)
+    assert torch.equal(a.o, b.o) and hils.hils_get_status() == 0
+
+
+def test_sequences_that_share_a_prefix():
+    """Two sequences whose tables name the same pages for their first chunks, with tails of their own: each decodes as
+    if it had the pages alone, and a step's append writes its own tail."""
+    loop = _Loop(True, B=2, seed=70)
+    loop.x[1, :128] = loop.x[0, :128]
+    loop.lq[1, :, :2] = loop.lq[0, :, :2]
+    alone = _Loop(True, B=2, seed=70)
+    alone.x.copy_(loop.x), alone.lq.copy_(loop.lq)
+    alone.prompt([140, 150])
+    # the shared form: the second sequence appends only what follows the prefix
+    loop.table[1, :2] = loop.table[0, :2]
+    rows = torch.cat([loop.x[0, :140], loop.x[1, 128:150]])
+    q, k, v = loop._split(rows)
+    loop.seqlens.copy_(torch.tensor([140, 150], dtype=torch.int32))
+    cu = torch.tensor([0, 140, 162], dtype=torch.int32, device="cuda")
+    hils.kv_append(loop.kp, loop.vp, loop.table, k, v, loop.seqlens, cu_tokens=cu, rotary=loop.rotary, q=q)
+    hils.landmark_summary_append(loop.kp, loop.table, loop.lq, loop.seqlens, 162, loop.summ, cu_tokens=cu)
+    for t in (loop.summ.kprime, loop.summ.bprime, loop.summ.kprime_mma.view(2, loop.Hkv, -1, loop.d + 16)):
+        t[1, :, :2] = t[0, :, :2]
+    loop.lens = [140, 150]
+    for _ in range(3):
+        for x in (loop, alone):
+            x.feed()
+            x.step()
+        assert torch.equal(loop.o, alone.o)
+    assert hils.hils_get_status() == 0
+
+
 def test_step_is_reproducible():
     m = _cache(4, 16, 4, 128, 4096, "bf16", seed=50)
     seq = torch.tensor([4096, 4000, 100, 2049], dtype=torch.int32, device="cuda")

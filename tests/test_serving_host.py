@@ -103,7 +103,7 @@ def test_rotary_refused(lib, ro):
     dict(table=BAD), dict(n=0), dict(k=rows(2, data=264)), dict(k=rows(2, ts=129)), dict(k=rows(2, hs=4)),
     dict(v=rows(2, ts=-128)), dict(q_out=rows(4, data=1 << 20, ts=0)), dict(q_out=rows(4, data=1 << 20, hs=0)),
     dict(q_out=rows(4, data=1 << 20, ts=64, hs=64)), dict(q_out=rows(4, data=1 << 20, ts=128, hs=64)),
-    dict(q_out=rows(4, data=1 << 20, ts=1 << 41)),
+    dict(k=rows(2, ts=1 << 61)), dict(q_out=rows(4, data=1 << 20, hs=1 << 61)), dict(v=rows(2, hs=1 << 62)),
 ])
 def test_rows_and_pages_refused(lib, kw):
     assert append(lib, **kw) == 1
