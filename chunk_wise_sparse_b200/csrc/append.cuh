@@ -6,6 +6,8 @@
 // tokens cu[b] .. cu[b+1]-1, which are its positions seqlens[b] - n_b ..
 // seqlens[b] - 1.
 #pragma once
+#include <type_traits>
+
 #include "quant.cuh"
 
 namespace hils {
@@ -113,6 +115,14 @@ __device__ __forceinline__ void widen(uint4 w, float (&x)[Vec16<T>::E]) {
   }
 }
 
+// E fp32 values rounded to the type.
+template <typename T>
+__device__ __forceinline__ uint4 narrow(const float (&x)[Vec16<T>::E]) {
+  uint4 w;
+  Vec16<T>::store(reinterpret_cast<T*>(&w), x);
+  return w;
+}
+
 // One warp per (token, share of its rows).  A row (one head of q, k or v) is
 // held by LPR = d / E lanes, a 16-byte piece each, KPI = 32 / LPR rows at a
 // time; the token's place and the angles of the lane's dims are found once and
@@ -176,65 +186,80 @@ __global__ void __launch_bounds__(128, 8) kv_append_kernel(AppendParams p) {
       }
     }
   }
-  auto load = [&](int i0, uint4 (&w)[U]) {
+  // steps a .. b - 1 (of KPI heads each) of one kind of row
+  auto segment = [&](auto kind_, const RowsView& in, int heads, int a, int b) {
+    constexpr int KIND = decltype(kind_)::value;       // 0 query, 1 key, 2 value
+    constexpr bool CODES = Q4 && KIND > 0;
+    if (a >= b) return;
+    const T* src = static_cast<const T*>(in.data) + t * in.ts + int64_t(a * KPI + grp) * in.hs + dim0;
+    const int64_t next = int64_t(KPI) * in.hs;
+    // where head a KPI + grp goes, and how far apart the heads of two steps are (bytes)
+    uint8_t* dst;
+    int64_t dst_next;
+    if constexpr (KIND == 0) {
+      dst = reinterpret_cast<uint8_t*>(static_cast<T*>(p.q_out.data) + t * p.q_out.ts + int64_t(a * KPI + grp) * p.q_out.hs + dim0);
+      dst_next = int64_t(KPI) * p.q_out.hs * int64_t(sizeof(T));
+    } else {
+      constexpr int64_t BLOCK = CODES ? QuantPage<D>::BLOCK : int64_t(kChunk) * D * int64_t(sizeof(T));
+      dst = static_cast<uint8_t*>(KIND == 1 ? p.k_pages : p.v_pages) +
+            ((in_pool ? page : 0) * p.Hkv + a * KPI + grp) * BLOCK + (CODES ? 0 : (in_chunk * D + dim0) * int(sizeof(T)));
+      dst_next = KPI * BLOCK;
+    }
+    int left = heads - (a * KPI + grp);      // heads of this lane group from here on, counted in steps of KPI
+    uint4 w[U];
+    auto load = [&](uint4 (&x)[U], int ahead) {      // of steps `ahead` .. + U - 1 from src on
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int it = i0 + u;
-      const int kind = it < nq ? 0 : it < nq + nk ? 1 : 2;    // query, key, value
-      const int h = (it - (kind == 0 ? 0 : nq + (kind - 1) * nk)) * KPI + grp;
-      const RowsView& src = kind == 0 ? p.q : kind == 1 ? p.k : p.v;
-      w[u] = make_uint4(0, 0, 0, 0);
-      if (it < it1 && h < (kind == 0 ? p.Hq : p.Hkv))
-        w[u] = *reinterpret_cast<const uint4*>(static_cast<const T*>(src.data) + t * src.ts + h * src.hs + dim0);
+      for (int u = 0; u < U; ++u) {
+        x[u] = make_uint4(0, 0, 0, 0);
+        if (ahead + u < b - a && left > (ahead + u) * KPI) x[u] = *reinterpret_cast<const uint4*>(src + (ahead + u) * next);
+      }
+    };
+    load(w, 0);
+    for (; a < b; a += U) {
+      uint4 ahead[U];
+      load(ahead, U);     // of the next round, while this one is worked on
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (a + u >= b) break;
+        if (KIND < 2 && p.rot > 0) {
+          float x[E], z[E];
+          widen<T>(w[u], x);
+          if (p.interleaved) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) z[e] = x[e ^ 1];
+          } else {
+            uint4 o;
+            o.x = __shfl_sync(0xffffffffu, w[u].x, partner);
+            o.y = __shfl_sync(0xffffffffu, w[u].y, partner);
+            o.z = __shfl_sync(0xffffffffu, w[u].z, partner);
+            o.w = __shfl_sync(0xffffffffu, w[u].w, partner);
+            widen<T>(o, z);
+          }
+          if (turns) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) x[e] = fmaf(x[e], c[e], z[e] * s[e]);
+          }
+          if constexpr (CODES) quant_store_row<D, E>(x, sub, dst, in_chunk, left > u * KPI && in_pool);
+          else if (turns) w[u] = narrow<T>(x);
+        } else if constexpr (CODES) {
+          float x[E];
+          widen<T>(w[u], x);
+          quant_store_row<D, E>(x, sub, dst, in_chunk, left > u * KPI && in_pool);
+        }
+        if constexpr (!CODES)
+          if (left > u * KPI && (KIND == 0 || in_pool)) *reinterpret_cast<uint4*>(dst) = w[u];
+        dst += dst_next;
+      }
+      src += U * next;
+      left -= U * KPI;
+#pragma unroll
+      for (int u = 0; u < U; ++u) w[u] = ahead[u];
     }
   };
-  uint4 w[U];
-  load(it0, w);
-  for (int i0 = it0; i0 < it1; i0 += U) {
-    uint4 ahead[U];
-    load(i0 + U, ahead);     // of the next round, while this one is worked on
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int it = i0 + u;
-      if (it >= it1) break;
-      const int kind = it < nq ? 0 : it < nq + nk ? 1 : 2;
-      const int h = (it - (kind == 0 ? 0 : nq + (kind - 1) * nk)) * KPI + grp;
-      const bool live = h < (kind == 0 ? p.Hq : p.Hkv);
-      float x[E];
-      widen<T>(w[u], x);
-      if (p.rot > 0 && kind < 2) {
-        float z[E];
-        if (p.interleaved) {
-#pragma unroll
-          for (int e = 0; e < E; ++e) z[e] = x[e ^ 1];
-        } else {
-          uint4 o;
-          o.x = __shfl_sync(0xffffffffu, w[u].x, partner);
-          o.y = __shfl_sync(0xffffffffu, w[u].y, partner);
-          o.z = __shfl_sync(0xffffffffu, w[u].z, partner);
-          o.w = __shfl_sync(0xffffffffu, w[u].w, partner);
-          widen<T>(o, z);
-        }
-        if (turns) {
-#pragma unroll
-          for (int e = 0; e < E; ++e) x[e] = fmaf(x[e], c[e], z[e] * s[e]);
-        }
-      }
-      if (kind == 0) {
-        if (live) Vec16<T>::store(static_cast<T*>(p.q_out.data) + t * p.q_out.ts + h * p.q_out.hs + dim0, x);
-        continue;
-      }
-      void* pool = kind == 1 ? p.k_pages : p.v_pages;
-      const bool store = live && in_pool;
-      const int64_t row = store ? page * p.Hkv + h : 0;
-      if constexpr (Q4)
-        quant_store_row<D, E>(x, sub, static_cast<uint8_t*>(pool) + row * QuantPage<D>::BLOCK, in_chunk, store);
-      else if (store)
-        Vec16<T>::store(static_cast<T*>(pool) + (row * kChunk + in_chunk) * D + dim0, x);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) w[u] = ahead[u];
-  }
+  auto clip = [](int x, int n) { return x < 0 ? 0 : x < n ? x : n; };
+  segment(std::integral_constant<int, 0>{}, p.q, p.Hq, clip(it0, nq), clip(it1, nq));
+  segment(std::integral_constant<int, 1>{}, p.k, p.Hkv, clip(it0 - nq, nk), clip(it1 - nq, nk));
+  segment(std::integral_constant<int, 2>{}, p.v, p.Hkv, clip(it0 - nq - nk, nk), clip(it1 - nq - nk, nk));
 }
 
 struct ReadParams {
