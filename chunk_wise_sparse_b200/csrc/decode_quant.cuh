@@ -13,6 +13,20 @@
 
 namespace hils {
 
+// Loads of what the kernel before wrote, after pdl_wait(): the compiler may
+// move a plain load of constant memory (const __restrict__, __ldg) above the
+// wait, because it takes that memory for unchanging while the kernel runs.
+__device__ __forceinline__ float load_late(const float* p) {
+  float v;
+  asm volatile("ld.global.cg.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 load_late4(const float* p) {
+  float4 v;
+  asm volatile("ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p) : "memory");
+  return v;
+}
+
 // ---------------------------------------------------------------- Q1
 // One warp scores 16 chunks against the query heads of a kv head, eight heads
 // per matrix instruction (rows: chunks, columns: heads).  The order of the
@@ -146,7 +160,7 @@ __device__ __forceinline__ uint32_t warp_kth_key(const uint32_t (&v)[R], int K) 
 // A kept chunk's page is looked up here, by the thread that keeps it.
 template <int IT, int NT>
 __global__ void __launch_bounds__(NT)
-quant_topk_kernel(const float* __restrict__ ws_scores, const int32_t* __restrict__ seqlens, int64_t cap, int64_t nc,
+quant_topk_kernel(const float* ws_scores, const int32_t* __restrict__ seqlens, int64_t cap, int64_t nc,
                   int Hq, int K, const int32_t* __restrict__ table, int64_t n_pages, Kept* __restrict__ kept,
                   int32_t* __restrict__ ids_out, float* __restrict__ scores_out, int wm1) {
   constexpr int NW = NT / 32;
@@ -176,7 +190,7 @@ quant_topk_kernel(const float* __restrict__ ws_scores, const int32_t* __restrict
     kept[at + slot] = Kept{id, page, s, 0};
   };
   if (n <= K) {
-    for (int t = tid; t < K; t += NT) put(t, t < n ? t : -1, t < n ? sc[t] : -INFINITY);
+    for (int t = tid; t < K; t += NT) put(t, t < n ? t : -1, t < n ? load_late(sc + t) : -INFINITY);
     return;
   }
   const int64_t seg = IT > 0 ? ((n + NT - 1) / NT + 3) / 4 * 4 : (n + NT - 1) / NT;
@@ -190,12 +204,12 @@ quant_topk_kernel(const float* __restrict__ ws_scores, const int32_t* __restrict
     for (int e = 0; e < IT; e += 4) {
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       if (vec && e + 4 <= cnt) {
-        v = *reinterpret_cast<const float4*>(sc + s0 + e);
+        v = load_late4(sc + s0 + e);
       } else {
-        if (e < cnt) v.x = sc[s0 + e];
-        if (e + 1 < cnt) v.y = sc[s0 + e + 1];
-        if (e + 2 < cnt) v.z = sc[s0 + e + 2];
-        if (e + 3 < cnt) v.w = sc[s0 + e + 3];
+        if (e < cnt) v.x = load_late(sc + s0 + e);
+        if (e + 1 < cnt) v.y = load_late(sc + s0 + e + 1);
+        if (e + 2 < cnt) v.z = load_late(sc + s0 + e + 2);
+        if (e + 3 < cnt) v.w = load_late(sc + s0 + e + 3);
       }
       // key 0, which no score has (it is the image of a negative NaN of all
       // ones), marks the places behind the end
@@ -205,7 +219,7 @@ quant_topk_kernel(const float* __restrict__ ws_scores, const int32_t* __restrict
       key[e + 3] = e + 3 < cnt ? max(order_key(v.w), 1u) : 0u;
     }
   }
-  auto key_at = [&](int64_t e) { return max(order_key(sc[s0 + e]), 1u); };
+  auto key_at = [&](int64_t e) { return max(order_key(load_late(sc + s0 + e)), 1u); };
   auto for_keys = [&](auto f) {   // over this thread's keys (and, with IT > 0, zeros behind them)
     if constexpr (IT > 0) {
 #pragma unroll
@@ -350,7 +364,7 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kQdWarps * 32, 2)
 quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, const uint8_t* __restrict__ vpg,
                     const int32_t* __restrict__ table, int64_t n_pages, const int32_t* __restrict__ seqlens,
-                    int64_t cap, int Hq, int G, int Hkv, int K, float tau, const Kept* __restrict__ kept,
+                    int64_t cap, int Hq, int G, int Hkv, int K, float tau, const Kept* kept,
                     T* __restrict__ o, int n_oct, int wm1) {
   using A = QuantAttend<D>;
   using P = QuantPage<D>;
@@ -472,7 +486,8 @@ quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, co
     const int pair = tid + e * TH;
     mine[e] = make_int4(-1, -1, 0, 0);
     if (pair < n_sel) {
-      mine[e] = __ldg(reinterpret_cast<const int4*>(kept + row0 * K + pair));
+      const float4 k = load_late4(reinterpret_cast<const float*>(kept + row0 * K + pair));
+      mine[e] = make_int4(__float_as_int(k.x), __float_as_int(k.y), __float_as_int(k.z), 0);
       ids[pair] = uint32_t(mine[e].x);
       scs[pair] = __int_as_float(mine[e].z) * kLog2e;
     }
@@ -506,20 +521,26 @@ quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, co
       if (!owner) record_error(HILS_ERR_DEVICE_BOUNDS);
 #pragma unroll 1
       for (int q = 0; q < GV; q += 4) {
-        const uint32_t* list = ids + q * K;
+        const uint32_t* list[4];       // a head behind the last: the last's again
         int at[4] = {0, 0, 0, 0};
-#pragma unroll 1
-        for (int st = kMaxTopK; st > 0; st >>= 1)
 #pragma unroll
-          for (int g = 0; g < 4; ++g)
-            if (q + g < GV && at[g] + st <= K && list[g * K + at[g] + st - 1] < c) at[g] += st;
+        for (int g = 0; g < 4; ++g) list[g] = ids + (q + g < GV ? q + g : GV - 1) * K;
+        // no branches: four loads in flight per step
+#pragma unroll 1
+        for (int st = 1 << (31 - __clz(K)); st > 0; st >>= 1)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const int to = at[g] + st;
+            const uint32_t v = list[g][(to < K ? to : K) - 1];
+            at[g] = (to <= K) & (v < c) ? to : at[g];
+          }
         uint32_t four = 0xFFFFFFFFu;
 #pragma unroll
-        for (int g = 0; g < 4; ++g)
-          if (q + g < GV && at[g] < K && list[g * K + at[g]] == c) {
-            four ^= uint32_t(0xFF ^ at[g]) << (8 * g);
-            if (q + g < g_own) owner = false;
-          }
+        for (int g = 0; g < 4; ++g) {
+          const bool has = (q + g < GV) & (at[g] < K) & (list[g][at[g] < K ? at[g] : K - 1] == c);
+          four ^= has ? uint32_t(0xFF ^ at[g]) << (8 * g) : 0u;
+          owner = owner & !(has & (q + g < g_own));
+        }
         if (q == 0) place[0] = four; else place[1] = four;
       }
       if (owner) *reinterpret_cast<uint2*>(spot + pair * 8) = make_uint2(place[0], place[1]);
