@@ -128,13 +128,14 @@ __device__ __forceinline__ uint4 narrow(const float (&x)[Vec16<T>::E]) {
 // time; the token's place and the angles of the lane's dims are found once and
 // used for all rows of the warp.  y = x c + x' s' with x' the other element of
 // the pair (another lane's in the half-split style, fetched by a shuffle).
-// The kinds of row are padded to KPI rows each, so that the warp always works
-// on one kind.  HBM-bound for a prompt: two pieces per lane are loaded while
-// two are worked on, at 64 registers and 32 warps per SM.  Measured on a 32K
-// prompt of 16 + 2 x 16 heads of 64 dims (407 MB): 80 us, 5.1 TB/s; four
-// pieces without looking ahead 82 us, the same at 72 registers 94 us, four
-// ahead 98 us, warps of 8 steps instead of up to 32 90 us, one CTA per token
-// with the place found by every thread 178 us.
+// The kinds of row are padded to KPI rows each and have a straight loop each.
+// For a prompt bound by the latency of its loads: two pieces per lane are loaded
+// while two are worked on, at 64 registers and 32 warps per SM.  Measured on a
+// 32K prompt of 16 + 2 x 16 heads of 64 dims (407 MB): 79 us, 5.1 TB/s, 78 % of
+// a copy's rate; one loop that tells the kinds apart 81 us, four pieces
+// without looking ahead 82 us, three ahead 85 us, 51 registers 96 us, one CTA
+// per token with the place found by every thread 178 us.  Into 4 bits, 13.9K
+// ragged tokens of 32 + 2 x 8 heads of 128 dims (306 MB): about 72 us.
 constexpr int kAppendUnroll = 2;
 constexpr int kAppendSteps = 32;      // of KPI rows, per warp, where tokens abound
 
@@ -274,7 +275,8 @@ struct ReadParams {
 // One warp per (eight packed tokens, share of the heads): four lanes per token
 // read d / 8 bytes of codes each, which are eight neighbouring dims of every
 // group, and store those as one piece per group.  HBM-bound: 5 d / 8 bytes in,
-// d elements out per row.
+// d elements out per row; 128K tokens of 8 kv heads of 128 dims (705 MB): 124 us,
+// 5.7 TB/s, 87 % of a copy's rate.  A CTA per token with two-byte loads: 221 us.
 template <typename T, int D>
 __global__ void __launch_bounds__(128) kv_read_quant_kernel(ReadParams p) {
   using P = QuantPage<D>;

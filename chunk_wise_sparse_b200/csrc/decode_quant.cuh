@@ -33,7 +33,9 @@ __device__ __forceinline__ float4 load_late4(const float* p) {
 // dims inside the sum is free, so each lane reads its operand rows in 16-byte
 // pieces (row lane/4 and lane/4 + 8, piece 4 c + lane % 4) and the queries in
 // the same order: no shared memory, all loads of the 16 rows in flight at
-// once.  HBM-bound: (d + 16) x 2 bytes per (kv head, candidate).
+// once.  HBM-bound: (d + 16) x 2 bytes per (kv head, candidate); 8 x 128K with
+// 8 kv heads (38 MB): 10.3 us alone and cold, where a thread per candidate with
+// the rows staged in shared memory takes 15.8.
 template <int D>
 __global__ void __launch_bounds__(128)
 quant_scores_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ kmma,
@@ -336,13 +338,22 @@ quant_topk_kernel(const float* ws_scores, const int32_t* __restrict__ seqlens, i
 //     queries on the tensor cores, exactly, summed in fp32 per group of 32 dims:
 //     acc_jg = sum_{i in g} q_i code_ji; then
 //     z = tau sum_g [ s_jg acc_jg + m_jg sum_{i in g} q_i ].
-//   output (dims x heads): the codes in the same form times fp16(w_j s_jg); and m_jg times fp16(w_j), one instruction for all
-//     groups; w_j = e^(z_j - lse) e^(u - M) carries the fusion weight.  Rounding
-//     the weights to fp16 costs 2^-12 of each, an eighth of a bf16 output's.
+//   output (dims x heads): the codes in the same form times fp16(w_j s_jg), and
+//     m_jg times fp16(w_j), one instruction for all groups; w_j = e^(z_j - lse)
+//     e^(u - M) carries the fusion weight.  Rounding the weights to fp16 costs
+//     2^-12 of each, an eighth of a bf16 output's half step of 2^-9.
 // fp32 models: queries, and the weights times s and m, as sums of three bf16
 // values (24 bits), so that the products are fp32's.
 // Running maximum, sum and outputs stay in registers over a warp's chunks;
 // warps merge in shared memory, CTAs through distributed shared memory.
+// Bound by instruction issue inside a chunk (1600 per chunk, issue slots 80 %
+// busy) and by what surrounds it: the first chunks of all warps arrive together
+// (3.8 us), and a warp has two chunks or three.  8 sequences of 128K, 64 chunks
+// per kv head: 24 us of the step's 42 (its 42 MB would take 6.4).  Measured for
+// the whole step: a lane per dims and a warp per (head, slot) on CUDA cores
+// 118 us; four warps per chunk instead of one 55 (each repeats the softmax and
+// the fusion: 2900 instructions per chunk); codes widened to bf16 16 + code
+// 47; slots in place of the list of distinct chunks 63.
 constexpr int kQdWarps = 8;
 
 template <int D> struct QuantAttend {

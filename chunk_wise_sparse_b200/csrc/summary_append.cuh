@@ -72,7 +72,9 @@ __device__ __forceinline__ void write_summary(const SummaryParams& p, int64_t un
 
 // Keys in the cache's own type: D / E lanes per key row.  Each warp's 16 keys
 // are loaded at once; their logits' maximum comes before any exponential, so
-// the sums need no rescaling inside a warp.
+// the sums need no rescaling inside a warp.  A step of 64 sequences of which
+// four complete a chunk (8 kv heads of 128 dims): 6.2 us in a graph, of which a
+// launch is about 4; a warp per chunk with four rows in flight took 14.4.
 template <typename T, int D>
 __global__ void __launch_bounds__(128) summary_append_kernel(SummaryParams p) {
   constexpr int E = Vec16<T>::E, LPK = D / E, KPI = 32 / LPK, ITERS = 16 / KPI;

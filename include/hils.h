@@ -455,8 +455,12 @@ size_t hils_decode_quant_workspace_bytes(const hils_dims* dims);
  *   q_score  scoring query as in hils_attn_decode_qcal, or NULL: q scores
  *   k_pages, v_pages, page_table, n_pages  as hils_kv_append_quant fills them
  *   workspace  at least hils_decode_quant_workspace_bytes(dims)
+ * bf16: queries and codes are multiplied exactly, the attention weights are
+ * rounded to fp16, sums are fp32; fp32: products of 24 bits throughout.
  * Other arguments, results and errors as in hils_attn_decode_paged;
- * B * Hkv <= 65535.
+ * B * Hkv * ceil(Hq / (8 Hkv)) <= 65535 (HILS_ERR_UNSUPPORTED otherwise).
+ * Three kernels, the last two ordered by programmatic stream serialisation as
+ * in hils_attn_decode.
  */
 int hils_attn_decode_quant(const hils_dims* dims, const void* q, const void* q_score, const void* k_pages,
                            const void* v_pages, const int32_t* page_table, int64_t n_pages, const float* kprime,
