@@ -356,7 +356,7 @@ typedef struct hils_rows {
 
 /* Rotary position table: fp32 [n_pos, rot_dim], for each position rot_dim/2
  * cosines and then rot_dim/2 sines.  The first rot_dim dims of every query
- * and key head are rotated, the rest carry no position ([AIT-Meth]: HoPE keeps
+ * and key head are rotated, the rest carry no position ([AIT-Tech]: HoPE keeps
  * part of the rotation).  rot_dim: a multiple of 16, 16 .. d. */
 typedef struct hils_rotary {
   const float* table;

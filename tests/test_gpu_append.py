@@ -115,6 +115,42 @@ def test_append_in_place_without_cu_and_head_major():
     assert hils.hils_get_status() == 0
 
 
+@pytest.mark.parametrize("B", [31, 32, 33, 1024, 1025, 3000])
+def test_many_sequences(B):
+    """Batches around the steps of the search for a token's sequence, of sequences with no, one or several new tokens:
+    every row lands where the plain placing says, in both kinds of page, and is read back from there."""
+    rng = np.random.default_rng(B)
+    cap, d = 128, 64
+    new = rng.integers(0, 3, B)
+    new[rng.integers(0, B, 5)] = 40
+    lens = np.minimum(cap, new + rng.integers(0, cap, B))
+    m = _make(torch.bfloat16, 1, 1, d, seqlens=lens, new=new, cap=cap, seed=B)
+    kp, vp = (torch.zeros((m["n_pages"], 1, C, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    hils.kv_append(kp, vp, m["table"], m["k"], m["v"], m["seqlens"], cu_tokens=m["cu"])
+    at = np.array(ref.places(lens.tolist(), m["cu_host"].tolist()))
+    page = torch.from_numpy(m["table_host"][at[:, 1], at[:, 2] // C].astype(np.int64)).cuda()
+    row = torch.from_numpy(at[:, 2] % C).cuda()
+    want_k, want_v = torch.zeros_like(kp), torch.zeros_like(vp)
+    want_k[page, :, row], want_v[page, :, row] = m["k"], m["v"]
+    assert torch.equal(kp, want_k) and torch.equal(vp, want_v)
+    k4, v4 = hils.quant_pages(m["n_pages"], 1, d), hils.quant_pages(m["n_pages"], 1, d)
+    hils.kv_append(k4, v4, m["table"], m["k"], m["v"], m["seqlens"], cu_tokens=m["cu"])
+    k, v = hils.kv_read(k4, v4, m["table"], m["seqlens"], m["T"], torch.bfloat16, cu_tokens=m["cu"])
+    assert hils.hils_get_status() == 0
+    for got, x in ((k, m["k"]), (v, m["v"])):
+        x = x.float()
+        # half a step of the group's range, the roundings of its ends to fp16 and of the value to bf16
+        g = x.view(*x.shape[:2], -1, 32)
+        step = (g.amax(-1) - g.amin(-1)) / 15
+        tol = (0.5 * step + 2.0 ** -10 * g.abs().amax(-1))[..., None] + 2.0 ** -8 * g.abs() + 2.0 ** -8 * step[..., None]
+        assert bool(((got.float().view(g.shape) - g).abs() <= tol).all())
+    # one of the two alone
+    only = torch.zeros_like(k)
+    dims = hils.make_dims(B, 1, 1, d, cap, 1, torch.bfloat16)
+    hils.hils_kv_read_quant(dims, m["seqlens"], m["T"], m["cu"], None, v4, m["table"], m["n_pages"], None, only)
+    assert torch.equal(only, v) and hils.hils_get_status() == 0
+
+
 def test_append_far_positions():
     """Positions near the end of a long sequence: offsets of the page pool beyond 2^31 elements, angles of 1e6."""
     d, H, cap = 128, 8, 1 << 20
