@@ -628,6 +628,8 @@ def _new(like, shape, dtype, stream):
     """A new tensor on the stream that the kernels will run on, so that the caching allocator gives its memory to no
     other stream's work before they end."""
     if stream is None:
+        if like.dtype is dtype and like.shape == shape:
+            return torch.empty_like(like, memory_format=torch.contiguous_format)
         return like.new_empty(shape, dtype=dtype)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
@@ -659,7 +661,7 @@ def kv_append(k_pages, v_pages, page_table, k, v, seqlens, cu_tokens=None, rotar
         Hq = q.shape[1]
         _need(q, "q", dtype, (T, Hq, d))
         if q_out is None:
-            q_out = _new(k, (T, Hq, d), dtype, stream)
+            q_out = _new(q, (T, Hq, d), dtype, stream)
         else:
             _need(q_out, "q_out", dtype, (T, Hq, d))
     elif q_out is not None:
