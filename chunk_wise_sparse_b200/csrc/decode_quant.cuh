@@ -115,10 +115,9 @@ struct __align__(16) Kept {
   int32_t pad;
 };
 
-// The largest key t of this warp's v[] (one value per lane and register, 0: no
-// value) with at least K of them >= t, or any t with exactly K; 1 if there are
-// fewer than K.  Bisection: first of the scores' interval (nine tenths of the
-// keys' is exponents of scores near zero), then of the keys'.
+// A score's place in the order; a NaN of either sign comes first, so that the
+// output of its row shows it.
+__device__ __forceinline__ uint32_t score_key(float s) { return s != s ? 0xFFFFFFFFu : order_key(s); }
 __device__ __forceinline__ float key_value(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k); }
 __device__ __forceinline__ uint32_t middle_key(uint32_t lo, uint32_t hi, int step) {
   const uint32_t d = hi - lo, mid = lo + (d >> 1) + (d & 1);
@@ -126,6 +125,10 @@ __device__ __forceinline__ uint32_t middle_key(uint32_t lo, uint32_t hi, int ste
   const uint32_t k = order_key(0.5f * key_value(lo) + 0.5f * key_value(hi));
   return k > lo && k <= hi ? k : mid;
 }
+// The largest key t of this warp's v[] (one value per lane and register, 0: no
+// value) with at least K of them >= t, or any t with exactly K; 1 if there are
+// fewer than K.  Bisection: first of the scores' interval (nine tenths of the
+// keys' is exponents of scores near zero), then of the keys'.
 template <int R>
 __device__ __forceinline__ uint32_t warp_kth_key(const uint32_t (&v)[R], int K) {
   uint32_t lo = 0xFFFFFFFFu, hi = 0u, some = 0;
@@ -213,15 +216,14 @@ quant_topk_kernel(const float* ws_scores, const int32_t* __restrict__ seqlens, i
         if (e + 2 < cnt) v.z = load_late(sc + s0 + e + 2);
         if (e + 3 < cnt) v.w = load_late(sc + s0 + e + 3);
       }
-      // key 0, which no score has (it is the image of a negative NaN of all
-      // ones), marks the places behind the end
-      key[e] = e < cnt ? max(order_key(v.x), 1u) : 0u;
-      key[e + 1] = e + 1 < cnt ? max(order_key(v.y), 1u) : 0u;
-      key[e + 2] = e + 2 < cnt ? max(order_key(v.z), 1u) : 0u;
-      key[e + 3] = e + 3 < cnt ? max(order_key(v.w), 1u) : 0u;
+      // key 0, which no score has, marks the places behind the end
+      key[e] = e < cnt ? score_key(v.x) : 0u;
+      key[e + 1] = e + 1 < cnt ? score_key(v.y) : 0u;
+      key[e + 2] = e + 2 < cnt ? score_key(v.z) : 0u;
+      key[e + 3] = e + 3 < cnt ? score_key(v.w) : 0u;
     }
   }
-  auto key_at = [&](int64_t e) { return max(order_key(load_late(sc + s0 + e)), 1u); };
+  auto key_at = [&](int64_t e) { return score_key(load_late(sc + s0 + e)); };
   auto for_keys = [&](auto f) {   // over this thread's keys (and, with IT > 0, zeros behind them)
     if constexpr (IT > 0) {
 #pragma unroll
@@ -531,11 +533,11 @@ quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, co
       owner = int64_t(mine[e].x) < n_cand;
       if (!owner) record_error(HILS_ERR_DEVICE_BOUNDS);
 #pragma unroll 1
-      for (int q = 0; q < GV; q += 4) {
+      for (int f = 0; f < GV; f += 4) {
         const uint32_t* list[4];       // a head behind the last: the last's again
         int at[4] = {0, 0, 0, 0};
 #pragma unroll
-        for (int g = 0; g < 4; ++g) list[g] = ids + (q + g < GV ? q + g : GV - 1) * K;
+        for (int g = 0; g < 4; ++g) list[g] = ids + (f + g < GV ? f + g : GV - 1) * K;
         // no branches: four loads in flight per step
 #pragma unroll 1
         for (int st = 1 << (31 - __clz(K)); st > 0; st >>= 1)
@@ -548,11 +550,11 @@ quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, co
         uint32_t four = 0xFFFFFFFFu;
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          const bool has = (q + g < GV) & (at[g] < K) & (list[g][at[g] < K ? at[g] : K - 1] == c);
+          const bool has = (f + g < GV) & (at[g] < K) & (list[g][at[g] < K ? at[g] : K - 1] == c);
           four ^= has ? uint32_t(0xFF ^ at[g]) << (8 * g) : 0u;
-          owner = owner & !(has & (q + g < g_own));
+          owner = owner & !(has & (f + g < g_own));
         }
-        if (q == 0) place[0] = four; else place[1] = four;
+        if (f == 0) place[0] = four; else place[1] = four;
       }
       if (owner) *reinterpret_cast<uint2*>(spot + pair * 8) = make_uint2(place[0], place[1]);
     }
@@ -734,7 +736,7 @@ quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, co
       for (int x = 4; x < 32; x <<= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
       const bool kept = (cur.heads >> (2 * tig + e)) & 1u;
       const float u = cur.window ? m + log2f(l) : cur.u[e];
-      const float mn = kept ? fmaxf(M[e], u) : M[e];
+      const float mn = !kept ? M[e] : u != u ? u : fmaxf(M[e], u);      // a NaN score is not dropped
       alpha[e] = mn == -INFINITY ? 1.f : exp2f(M[e] - mn);
       const float beta = kept && mn != -INFINITY ? exp2f(u - mn) : 0.f;
       Z[e] = fmaf(Z[e], alpha[e], beta);

@@ -455,6 +455,7 @@ size_t hils_decode_quant_workspace_bytes(const hils_dims* dims);
  *   q_score  scoring query as in hils_attn_decode_qcal, or NULL: q scores
  *   k_pages, v_pages, page_table, n_pages  as hils_kv_append_quant fills them
  *   workspace  at least hils_decode_quant_workspace_bytes(dims)
+ * A chunk whose score is NaN is kept before all others, so that the NaN shows.
  * bf16: queries and codes are multiplied exactly, the attention weights are
  * rounded to fp16, sums are fp32; fp32: products of 24 bits throughout.
  * Other arguments, results and errors as in hils_attn_decode_paged;

@@ -154,6 +154,25 @@ def test_rows_behind_the_sequence_are_not_looked_at():
     assert not bool(bad.any())
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_nan_in_a_key_reaches_the_heads_that_read_it(dtype):
+    """A group of a cached key that stands for NaN makes its chunk's summary and scores NaN: they sort first, and the
+    kv head's query heads become NaN; the other kv head and the other sequence do not change."""
+    m = _cache(2, 6, 2, 64, 2048, dtype, seed=13)
+    seq = torch.tensor([2048, 2000], dtype=torch.int32, device="cuda")
+    args = (m["q"], m["kp"], m["vp"], m["table"], m["summ"], seq, 8)
+    want = hils.decode_step_quant(*args, window=128)[0].clone()
+    page = m["kp"][int(m["table_host"][0, 3])]
+    page[1, C * 32:].view(C, 8)[5, 4:] = 0xFF                      # sequence 0, kv head 1, chunk 3, key 5, dims 32 .. 63
+    full = torch.full((2,), 2048, dtype=torch.int32, device="cuda")
+    hils.landmark_summary_append(m["kp"], m["table"], m["lq"], full, 2 * 2048, m["summ"])
+    got, ids, _ = hils.decode_step_quant(*args, window=128, with_selection=True)
+    assert hils.hils_get_status() == 0
+    assert bool(torch.isnan(m["summ"].kprime[0, 1, 3]).all()) and bool((ids[0, 3:] == 3).any(-1).all())
+    assert bool(torch.isnan(got[0, 3:].float()).all())
+    assert torch.equal(got[0, :3], want[0, :3]) and torch.equal(got[1], want[1])
+
+
 def test_decode_records_bad_pages_and_lengths():
     m = _cache(3, 4, 2, 64, 1024, "bf16", seed=11)
     seq = torch.tensor([1024, 1000, 900], dtype=torch.int32, device="cuda")
