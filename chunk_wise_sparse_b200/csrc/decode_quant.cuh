@@ -348,15 +348,18 @@ quant_topk_kernel(const float* ws_scores, const int32_t* __restrict__ seqlens, i
 // values (24 bits), so that the products are fp32's.
 // Running maximum, sum and outputs stay in registers over a warp's chunks;
 // warps merge in shared memory, CTAs through distributed shared memory.
-// Bound by instruction issue inside a chunk (1600 per chunk, issue slots 80 %
-// busy) and by what surrounds it: the first chunks of all warps arrive together
-// (3.8 us), and a warp has two chunks or three.  8 sequences of 128K, 64 chunks
-// per kv head: 24 us of the step's 42 (its 42 MB would take 6.4).  Measured for
-// the whole step: a lane per dims and a warp per (head, slot) on CUDA cores
-// 118 us; four warps per chunk instead of one 55 (each repeats the softmax and
-// the fusion: 2900 instructions per chunk); codes widened to bf16 16 + code
-// 47; slots in place of the list of distinct chunks 63.
-constexpr int kQdWarps = 8;
+// Bound by instruction issue inside a chunk (about 1600) and by what surrounds
+// it: the first chunks of all warps arrive together (3.8 us), and a warp has
+// one chunk more or less than another.  8 sequences of 128K, 64 chunks per kv
+// head: 19 us of the step's 37.5 (its 42 MB would take 6.4).  Two CTAs of six
+// warps per SM, for 168 registers a thread: of eight (128 registers, spills)
+// 43 us for the step, seven 39.6, five 40.3, four 38.8, three of four 39.3, one
+// of eight 41.5.  Also measured, for the step at the time: a warp per (head,
+// slot) on CUDA cores 118 us; four warps per chunk instead of one 55 against 45
+// (each repeats the softmax and the fusion: 2900 instructions per chunk); codes
+// widened to bf16 16 + code 47; slots in place of the list of distinct chunks
+// 63 against 47.
+constexpr int kQdWarps = 6;
 
 template <int D> struct QuantAttend {
   static constexpr int BLOCK = int(QuantPage<D>::BLOCK);
@@ -482,7 +485,7 @@ quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, co
   const int64_t n_cand = own - wm1 > 0 ? own - wm1 : 0;
   const int n_sel = own < 0 ? 0 : GV * K;
   const int n_win = own < 0 ? 0 : int(own < wm1 ? own + 1 : wm1 + 1);
-  constexpr int TH = kQdWarps * 32, PER = A::LISTS / TH;      // kept pairs per thread, at most
+  constexpr int TH = kQdWarps * 32, PER = (A::LISTS + TH - 1) / TH;      // kept pairs per thread, at most
   // the window's pages do not depend on the selection
   int win_page = -1;
   if (tid < n_win) {

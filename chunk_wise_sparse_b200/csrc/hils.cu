@@ -1037,8 +1037,9 @@ int launch_decode_quant(const hils_dims* d, const void* q, const void* q_score, 
   // fewer have a chunk each already
   const int n_oct = (G + 7) / 8, heads = G < 8 ? G : 8;
   const int64_t groups = int64_t(bh) * n_oct, slots = int64_t(heads) * K + wm1 + 1;
-  unsigned cl = 1;
-  while (cl < 8 && int64_t(cl) * kQdWarps < slots && groups * cl * 2 <= 2 * sm_count()) cl *= 2;
+  const int64_t room = 2 * int64_t(sm_count()) / groups, want = (slots + kQdWarps - 1) / kQdWarps;
+  const int64_t fit = room < want ? room : want;
+  const unsigned cl = unsigned(fit < 1 ? 1 : fit > 8 ? 8 : fit);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(cl, unsigned(groups));
   cfg.blockDim = dim3(kQdWarps * 32);
