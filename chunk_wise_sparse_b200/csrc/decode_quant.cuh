@@ -371,8 +371,9 @@ template <int D> struct QuantAttend {
   static constexpr int PART = D + 4, INBOX = 15 * PART;
   static constexpr int LISTS = 8 * kMaxTopK;                  // kept (head, slot) pairs of a cluster, at most
   static constexpr int ITEMS = LISTS + 16;                    // distinct chunks and window chunks
-  // staging, the CTAs' sums of the heads this one finishes, scores of the pairs, places of a pair's chunk in
-  // the heads' lists, ids of the pairs, then the items' page and pair
+  // staging, the CTAs' sums of the heads this one finishes, scores of the pairs,
+  // places of a pair's chunk in the heads' lists, ids of the pairs, then the
+  // items' page and pair
   static constexpr int SMEM = kQdWarps * STAGE + INBOX * 4 + LISTS * (4 + 8 + 4) + ITEMS * 8;
 };
 
@@ -686,7 +687,7 @@ quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, co
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           if constexpr (NS == 1) codes_f16(cu[r][g / 2], cu[r][NG / 2 + g / 2], g & 1, a[r]);
-          else codes_bf16<true>(__byte_perm(cu[r][g / 2], cu[r][NG / 2 + g / 2], g & 1 ? 0x7632 : 0x5410), a[r]);
+          else codes_bf16_centred(__byte_perm(cu[r][g / 2], cu[r][NG / 2 + g / 2], g & 1 ? 0x7632 : 0x5410), a[r]);
         }
         if constexpr (NS == 1) {
           mma16816_f16_first(c, a[0][0], a[1][0], a[0][1], a[1][1], qb[0][g][0], qb[0][g][1]);
@@ -840,7 +841,7 @@ quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, co
           uint32_t a[2][4];
 #pragma unroll
           for (int r = 0; r < 2; ++r)
-            codes_bf16<true>(__byte_perm(vc[r][0][g / 2], vc[r][1][g / 2], g & 1 ? 0x7632 : 0x5410), a[r]);
+            codes_bf16_centred(__byte_perm(vc[r][0][g / 2], vc[r][1][g / 2], g & 1 ? 0x7632 : 0x5410), a[r]);
           // fresh sums per tile, added in fp32: the matrix unit's own sums are not rounded to nearest
           float c0[4] = {0.f, 0.f, 0.f, 0.f}, c1[4] = {0.f, 0.f, 0.f, 0.f}, cm[4] = {0.f, 0.f, 0.f, 0.f};
           constexpr uint32_t one = 0x3F803F80u;

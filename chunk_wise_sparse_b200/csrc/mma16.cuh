@@ -99,22 +99,18 @@ __device__ __forceinline__ void codes_f16_centred(uint32_t x, uint32_t y, bool u
   }
 }
 
-// Four codes of two 16-bit units as bf16 pairs: 16 + code has the code in
-// bits 3 .. 6.  CENTRE: code - 8 instead, exactly (one subtraction more; the
-// products' sums then do not carry the offset, which fp32 results would feel).
-template <bool CENTRE>
-__device__ __forceinline__ void codes_bf16(uint32_t x, uint32_t (&a)[4]) {
+// Four codes of two 16-bit units (one in each half of x) as bf16 pairs of
+// code - 8: 16 + code has the code in bits 3 .. 6, and 24 less is exact.
+__device__ __forceinline__ void codes_bf16_centred(uint32_t x, uint32_t (&a)[4]) {
   a[0] = ((x << 3) & 0x00780078u) | 0x41804180u;
   a[1] = ((x >> 1) & 0x00780078u) | 0x41804180u;
   a[2] = ((x >> 5) & 0x00780078u) | 0x41804180u;
   a[3] = ((x >> 9) & 0x00780078u) | 0x41804180u;
-  if constexpr (CENTRE) {
-    const __nv_bfloat162 c24 = __floats2bfloat162_rn(24.f, 24.f);
+  const __nv_bfloat162 c24 = __floats2bfloat162_rn(24.f, 24.f);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a[i]), c24);
-      a[i] = *reinterpret_cast<const uint32_t*>(&v);
-    }
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a[i]), c24);
+    a[i] = *reinterpret_cast<const uint32_t*>(&v);
   }
 }
 

@@ -31,19 +31,6 @@ template <int D> struct QuantPage {
   __host__ __device__ static constexpr int param_off(int row) { return kChunk * ROW + row * PROW; }
 };
 
-// Byte offset of the block of chunk c of (b, h), or -1 (recorded as
-// HILS_ERR_DEVICE_BOUNDS) when its page is outside the pool.
-template <int D>
-__device__ __forceinline__ int64_t quant_block_offset(const int32_t* table, int64_t n_pages, int64_t b, int64_t h,
-                                                      int64_t c, int64_t Hkv, int64_t nc) {
-  const int64_t page = __ldg(table + b * nc + c);
-  if (page < 0 || page >= n_pages) {
-    record_error(HILS_ERR_DEVICE_BOUNDS);
-    return -1;
-  }
-  return (page * Hkv + h) * QuantPage<D>::BLOCK;
-}
-
 // Quantise and store one row held by D / E neighbouring lanes of a warp, lane
 // `sub` of the row holding dims sub * E .. + E - 1 in fp32.  Every lane of the
 // warp takes part (shuffles); only those with `store` write.  A group with a
@@ -110,23 +97,6 @@ __device__ __forceinline__ void quant_store_row(const float (&x)[E], int sub, ui
     *reinterpret_cast<uint32_t*>(codes + 2 * (j * P::G + g)) = u[0] | (take << 16);
   }
   if (j == 0) *reinterpret_cast<__half2*>(block + P::param_off(row) + 4 * g) = par;
-}
-
-// E values of a row, dims sub * E .. + E - 1, in fp32.
-template <int D, int E>
-__device__ __forceinline__ void quant_load_row(const uint8_t* block, int row, int sub, float (&x)[E]) {
-  using P = QuantPage<D>;
-  constexpr int GL = kQGroup / E;
-  const int g = sub / GL, j = sub % GL;
-  const __half2 par = __ldg(reinterpret_cast<const __half2*>(block + P::param_off(row) + 4 * g));
-  const float s = __low2float(par), m = __high2float(par);
-#pragma unroll
-  for (int w = 0; w < E / 4; ++w) {
-    const int e = (E / 4) * j + w;
-    const uint32_t u = __ldg(reinterpret_cast<const uint16_t*>(block + P::code_off(row) + 2 * (e * P::G + g)));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[4 * w + i] = fmaf(s, float((u >> (4 * i)) & 15u), m);
-  }
 }
 
 }  // namespace hils
