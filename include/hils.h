@@ -374,7 +374,8 @@ typedef struct hils_rotary {
  *   tokens        the new tokens
  *   rotary        NULL: no rotation
  *   q, q_out      [T, Hq, d] (both NULL: no queries); q_out may be q itself
- *                 (same address and strides) but must not overlap it otherwise
+ *                 (same address and strides) but must not overlap it, k or v
+ *                 otherwise
  *   k, v          [T, Hkv, d]
  *   k_pages, v_pages  [n_pages, Hkv, C, d] dtype: the new positions' rows are
  *                 written, nothing else
