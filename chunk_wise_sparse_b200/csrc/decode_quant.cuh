@@ -340,10 +340,15 @@ quant_topk_kernel(const float* ws_scores, const int32_t* __restrict__ seqlens, i
 //     queries on the tensor cores, exactly, summed in fp32 per group of 32 dims:
 //     acc_jg = sum_{i in g} q_i code_ji; then
 //     z = tau sum_g [ s_jg acc_jg + m_jg sum_{i in g} q_i ].
-//   output (dims x heads): the codes in the same form times fp16(w_j s_jg), and
-//     m_jg times fp16(w_j), one instruction for all groups; w_j = e^(z_j - lse)
-//     e^(u - M) carries the fusion weight.  Rounding the weights to fp16 costs
-//     2^-12 of each, an eighth of a bf16 output's half step of 2^-9.
+//   output (dims x heads): the codes in the same form times W_j s_jg, and m_jg
+//     times W_j, one instruction for all groups; w_j = e^(z_j - lse) e^(u - M)
+//     carries the fusion weight, and W_j = 2^k w_j in fp16, with k such that the
+//     products with the largest step met so far lie below 2^15, and k <= 15, as
+//     w_j <= 1 (without it, weights of about 1/64 and steps below 4e-3 leave
+//     fp16's normal range, and values of 1e-4 were off by tens of percent).
+//     W_j and W_j s_jg are rounded to fp16, by 2^-11 of them each: together a
+//     quarter of a bf16 output's half step of 2^-8 for one key, and less for a
+//     sum over keys.
 // fp32 models: queries, and the weights times s and m, as sums of three bf16
 // values (24 bits), so that the products are fp32's.
 // Running maximum, sum and outputs stay in registers over a warp's chunks;
@@ -360,6 +365,16 @@ quant_topk_kernel(const float* ws_scores, const int32_t* __restrict__ seqlens, i
 // widened to bf16 16 + code 47; slots in place of the list of distinct chunks
 // 63 against 47.
 constexpr int kQdWarps = 6;
+
+// The power of two (its bits) that puts the largest step, given by its bits, in
+// [2^14, 2^15), but 2^15 at most: steps from 2^-1 to fp16's largest, of
+// exponent 15, have one of their own.
+constexpr uint32_t kWeightMost = uint32_t(127 + 15) << 23;
+__device__ __forceinline__ uint32_t weight_scale(uint32_t top) {
+  uint32_t e = top >> 23;
+  e = e < 126 ? 126 : e > 142 ? 142 : e;
+  return (268 - e) << 23;      // 2^(141 - e)
+}
 
 template <int D> struct QuantAttend {
   static constexpr int BLOCK = int(QuantPage<D>::BLOCK);
@@ -625,6 +640,7 @@ quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, co
   auto wait_all_but_one = [] { asm volatile("cp.async.wait_group 1;" ::: "memory"); };
 
   float acc[NG][2][4], least[2] = {0.f, 0.f}, M[2] = {-INFINITY, -INFINITY}, Z[2] = {0.f, 0.f};
+  uint32_t w_up = kWeightMost;      // NS == 1: 2^k, by which weights and sums are scaled
 #pragma unroll
   for (int i = 0; i < NG * 8; ++i) acc[i / 8][i / 4 % 2][i % 4] = 0.f;
 
@@ -747,14 +763,6 @@ quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, co
       coef[e] = kept ? beta / l : 0.f;
       M[e] = mn;
     }
-    if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
-#pragma unroll
-      for (int g = 0; g < NG; ++g)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) acc[g][i / 4][i % 4] *= alpha[i & 1];
-      least[0] *= alpha[0];
-      least[1] *= alpha[1];
-    }
     wait_all_but_one();
     __syncwarp();
     // ---- output
@@ -764,6 +772,35 @@ quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, co
 #pragma unroll
         for (int g = 0; g < NG; ++g) *reinterpret_cast<uint32_t*>(stage + A::BLOCK + P::param_off(key) + 4 * g) = 0u;
       __syncwarp();
+    }
+    if constexpr (NS == 1) {
+      // the largest step; a NaN is not the maximum of anything
+      const uint4* par = reinterpret_cast<const uint4*>(vst + P::param_off(0));
+      __half2 top = __floats2half2_rn(0.f, 0.f);       // in the lower half
+#pragma unroll
+      for (int i = 0; i < kChunk * P::PROW / 512; ++i) {
+        const uint4 u = par[lane + 32 * i];
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = __hmax2(top, *reinterpret_cast<const __half2*>(&w[e]));
+      }
+      const uint32_t up = weight_scale(__reduce_max_sync(0xffffffffu, __float_as_uint(__low2float(top))));
+      if (up < w_up) {      // powers of two: their bits compare as they do, and differ by the bits of the quotient's exponent
+        const float f = __uint_as_float(0x3F800000u - (w_up - up));
+        alpha[0] *= f;
+        alpha[1] *= f;
+        w_up = up;
+      }
+      coef[0] *= __uint_as_float(w_up);
+      coef[1] *= __uint_as_float(w_up);
+    }
+    if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+      for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[g][i / 4][i % 4] *= alpha[i & 1];
+      least[0] *= alpha[0];
+      least[1] *= alpha[1];
     }
     float lm[4] = {0.f, 0.f, 0.f, 0.f};      // the chunk's least values, one row per group
     const uint32_t kept_mask = (cur.heads >> gid) & 1u ? 0xFFFFFFFFu : 0u;   // of the column this lane feeds
@@ -877,15 +914,17 @@ quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, co
 
   // ---- the warp's sums to its stage: row per head, then (maximum, sum)
   float* sums = reinterpret_cast<float*>(stage);
+  const float w_down = NS == 1 ? __uint_as_float((254u << 23) - w_up) : 1.f;      // 2^-k
 #pragma unroll
   for (int g = 0; g < NG; ++g)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       float add = 0.f, f = 1.f, f4 = 1.f;
       if constexpr (NS == 1) {
-        add = __shfl_sync(0xffffffffu, least[e], 4 * g + tig);
-        f = 16777216.f;      // the codes were multiplied as code 2^-24, those of rows gid + 8 (odd dims) as code 2^-20
-        f4 = 1048576.f;
+        add = __shfl_sync(0xffffffffu, least[e], 4 * g + tig) * w_down;
+        // the codes were multiplied as code 2^-24, those of rows gid + 8 (odd dims) as code 2^-20
+        f = 16777216.f * w_down;
+        f4 = 1048576.f * w_down;
       }
       // dims 32 g + 4 gid + 0 .. 3
       *reinterpret_cast<float4*>(sums + (2 * tig + e) * A::RS + 32 * g + 4 * gid) =

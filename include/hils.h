@@ -457,8 +457,11 @@ size_t hils_decode_quant_workspace_bytes(const hils_dims* dims);
  *   k_pages, v_pages, page_table, n_pages  as hils_kv_append_quant fills them
  *   workspace  at least hils_decode_quant_workspace_bytes(dims)
  * A chunk whose score is NaN is kept before all others, so that the NaN shows.
- * bf16: queries and codes are multiplied exactly, the attention weights are
- * rounded to fp16, sums are fp32; fp32: products of 24 bits throughout.
+ * bf16: queries and codes are multiplied exactly; the attention weights
+ * (scaled by a power of two that follows the values' steps), and then their
+ * products with the steps, are rounded to fp16, by 2^-11 of them each; the sum
+ * of a query's 32 values of a group has 22 bits; sums are fp32.  fp32: products
+ * of 24 bits throughout.
  * Other arguments, results and errors as in hils_attn_decode_paged;
  * B * Hkv * ceil(Hq / (8 Hkv)) <= 65535 (HILS_ERR_UNSUPPORTED otherwise).
  * Three kernels, the last two ordered by programmatic stream serialisation as
