@@ -25,41 +25,48 @@ struct Place {
   int64_t b, pos;
 };
 
-__device__ __forceinline__ Place place_in(const TokenBatch& tb, int64_t t, int64_t b, int64_t lo, int64_t hi) {
-  Place p{-1, 0};
-  const int64_t len = __ldg(tb.seqlens + b), start = len - (hi - lo);
-  if (lo < 0 || t < lo || t >= hi || start < 0 || len > tb.cap) {
-    record_error(HILS_ERR_DEVICE_BOUNDS);
-    return p;
+// The place of token t as one of sequence b's, where the last sequence ends at
+// `end`.  A sequence that reaches beyond the packed tokens, or whose neighbours'
+// tokens do not precede and follow its own, has no places: counted from a wrong
+// border its tokens would land on other positions than theirs, over rows that
+// the cache already holds.  All loads at once: a decode step waits for them.
+__device__ __forceinline__ Place place_in(const TokenBatch& tb, int64_t t, int64_t b, int64_t end) {
+  const int64_t len = __ldg(tb.seqlens + b);
+  int64_t lo = b * tb.per, hi = lo + tb.per;
+  bool bad = false;
+  if (tb.cu != nullptr) {
+    const int before = __ldg(tb.cu + (b > 0 ? b - 1 : 0)), after = __ldg(tb.cu + (b + 2 < tb.batch ? b + 2 : tb.batch));
+    lo = __ldg(tb.cu + b);
+    hi = __ldg(tb.cu + b + 1);
+    bad = (b == 0 ? lo != 0 : lo < 0) | (before > lo) | (after < hi);
   }
-  p.b = b;
-  p.pos = start + (t - lo);
-  return p;
+  const int64_t start = len - (hi - lo);
+  bad |= (t < lo) | (t >= hi) | (hi > end) | (hi > tb.n_tokens) | (start < 0) | (len > tb.cap);
+  if (bad) {
+    record_error(HILS_ERR_DEVICE_BOUNDS);
+    return Place{-1, 0};
+  }
+  return Place{b, start + (t - lo)};
 }
 
 // The place of token t, found by one thread.
 __device__ __forceinline__ Place find_place(const TokenBatch& tb, int64_t t) {
-  if (tb.cu == nullptr) {
-    const int64_t b = t / tb.per;
-    return place_in(tb, t, b, b * tb.per, (b + 1) * tb.per);
-  }
-  if (t >= __ldg(tb.cu + tb.batch)) return Place{-1, 0};   // padding
+  if (tb.cu == nullptr) return place_in(tb, t, t / tb.per, tb.n_tokens);
+  const int end = __ldg(tb.cu + tb.batch);
+  if (t >= end) return Place{-1, 0};   // padding
   int64_t lo = 0, hi = tb.batch;       // the last b with cu[b] <= t
   while (hi - lo > 1) {
     const int64_t mid = (lo + hi) >> 1;
     if (__ldg(tb.cu + mid) <= t) lo = mid; else hi = mid;
   }
-  return place_in(tb, t, lo, __ldg(tb.cu + lo), __ldg(tb.cu + lo + 1));
+  return place_in(tb, t, lo, end);
 }
 
 // The place of token t (the same for the whole warp): the last b with
 // cu[b] <= t by a 32-way search, one load per lane and round, so that a batch
 // of up to 32 sequences costs one load latency and one of up to 1024 two.
 __device__ __forceinline__ Place find_place_warp(const TokenBatch& tb, int64_t t, int lane) {
-  if (tb.cu == nullptr) {
-    const int64_t b = t / tb.per;
-    return place_in(tb, t, b, b * tb.per, (b + 1) * tb.per);
-  }
+  if (tb.cu == nullptr) return place_in(tb, t, t / tb.per, tb.n_tokens);
   const int end = __ldg(tb.cu + tb.batch);
   int lo = 0, len = tb.batch;
   while (len > 1) {
@@ -71,7 +78,7 @@ __device__ __forceinline__ Place find_place_warp(const TokenBatch& tb, int64_t t
     len = len - skip < step ? len - skip : step;
   }
   if (t >= end) return Place{-1, 0};     // padding
-  return place_in(tb, t, lo, __ldg(tb.cu + lo), __ldg(tb.cu + lo + 1));
+  return place_in(tb, t, lo, end);
 }
 
 // One block (or warp) of a launch looks at the whole of cu_tokens: it has to

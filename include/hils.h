@@ -381,10 +381,12 @@ typedef struct hils_rotary {
  *                 written, nothing else
  *   page_table    device int32 [B, seqlen/C]; the chunks of the new positions
  *                 must have pages, no two of them the same page
- * A token whose sequence description does not fit (seqlens[b] above the
- * capacity or below n_b, cu_tokens not ascending or beyond T, a position
- * outside the rotary table) is skipped; of one whose page is outside the pool
- * only the query is written.  Both are recorded as HILS_ERR_DEVICE_BOUNDS.
+ * The tokens of a sequence whose description does not fit (seqlens[b] above
+ * the capacity or below n_b; cu_tokens[b+1] beyond T or beyond cu_tokens[B];
+ * cu_tokens[0] not 0; cu_tokens[b-1] .. cu_tokens[b+2] not ascending) are
+ * skipped, and so is a token at a position outside the rotary table; of one
+ * whose page is outside the pool only the query is written.  All are recorded
+ * as HILS_ERR_DEVICE_BOUNDS, a descent anywhere in cu_tokens included.
  */
 int hils_kv_append_paged(const hils_dims* dims, const hils_tokens* tokens, const hils_rotary* rotary,
                          const hils_rows* q, const hils_rows* q_out, const hils_rows* k, const hils_rows* v,
