@@ -43,6 +43,29 @@ namespace hils {
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// What the kernel before wrote, as a kernel parameter, read after pdl_wait().
+// Its loads are volatile assembly, which stays behind the wait.  A plain load
+// of memory that the compiler takes for unchanging while the kernel runs
+// (const __restrict__, __ldg) may be moved above the wait, and then reads what
+// was there before.
+template <typename T> struct Late {
+  static_assert(sizeof(T) == 4 || sizeof(T) == 16, "one 32-bit or 128-bit load");
+  const T* p;
+  __device__ __forceinline__ T operator[](int64_t i) const {
+    union { uint32_t w[sizeof(T) / 4]; T v; } x;
+    if constexpr (sizeof(T) == 4)
+      asm volatile("ld.global.b32 %0, [%1];" : "=r"(x.w[0]) : "l"(p + i));
+    else
+      asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(x.w[0]), "=r"(x.w[1 % (sizeof(T) / 4)]), "=r"(x.w[2 % (sizeof(T) / 4)]), "=r"(x.w[3 % (sizeof(T) / 4)])
+                   : "l"(p + i));
+    return x.v;
+  }
+  // elements i .. as one wider value (aligned to it)
+  template <typename V> __device__ __forceinline__ V wide(int64_t i) const { return Late<V>{reinterpret_cast<const V*>(p + i)}[0]; }
+  __device__ __forceinline__ Late operator+(int64_t i) const { return Late{p + i}; }
+};
+
 struct DecodeWs {
   float* scores;      // [B*Hq, nc]
   int32_t* sel_ids;   // [B*Hq, K]
@@ -213,7 +236,7 @@ __device__ __forceinline__ int block_exclusive_scan256(int x, int* warp_tot, int
 }
 
 __global__ void __launch_bounds__(256)
-decode_topk_kernel(const float* __restrict__ ws_scores, const int32_t* __restrict__ seqlens, int64_t cap,
+decode_topk_kernel(Late<float> ws_scores, const int32_t* __restrict__ seqlens, int64_t cap,
                    int64_t nc, int Hq, int K, int32_t* __restrict__ sel_ids, float* __restrict__ sel_scores,
                    int wm1) {
   __shared__ uint32_t hist[256];
@@ -224,7 +247,7 @@ decode_topk_kernel(const float* __restrict__ ws_scores, const int32_t* __restric
   const int row = blockIdx.x, b = row / Hq, tid = threadIdx.x;
   int64_t n = decode_own_chunk(seqlens, b, cap) - wm1;   // candidates
   if (n < 0) n = 0;
-  const float* sc = ws_scores + int64_t(row) * nc;
+  const Late<float> sc = ws_scores + int64_t(row) * nc;
   int32_t* oid = sel_ids + int64_t(row) * K;
   float* osc = sel_scores + int64_t(row) * K;
   if (n <= K) {
@@ -240,9 +263,19 @@ decode_topk_kernel(const float* __restrict__ ws_scores, const int32_t* __restric
     const int shift = 24 - 8 * pass;
     hist[tid] = 0;
     __syncthreads();
-    for (int64_t c = tid; c < n; c += 256) {
-      const uint32_t key = order_key(sc[c]);
-      if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & 255u], 1u);
+    float s[4];      // the next four, loaded ahead
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[j] = tid + 256 * j < n ? sc[tid + 256 * j] : 0.f;
+    for (int64_t c = tid; c < n; c += 4 * 256) {
+      uint32_t key[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        key[j] = order_key(s[j]);
+        if (c + 256 * (j + 4) < n) s[j] = sc[c + 256 * (j + 4)];
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (c + 256 * j < n && (key[j] & mask) == prefix) atomicAdd(&hist[(key[j] >> shift) & 255u], 1u);
     }
     __syncthreads();
     if (tid < 32) {
@@ -276,10 +309,16 @@ decode_topk_kernel(const float* __restrict__ ws_scores, const int32_t* __restric
   const int64_t seg = (n + 255) / 256;
   const int64_t s0 = tid * seg, s1 = (s0 + seg < n) ? s0 + seg : n;
   int gt = 0, eq = 0;
-  for (int64_t c = s0; c < s1; ++c) {
-    const uint32_t key = order_key(sc[c]);
-    gt += key > prefix;
-    eq += key == prefix;
+  for (int64_t c = s0; c < s1; c += 4) {
+    float s[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[j] = sc[c + j < s1 ? c + j : s1 - 1];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t key = order_key(s[j]);
+      gt += c + j < s1 && key > prefix;
+      eq += c + j < s1 && key == prefix;
+    }
   }
   int tot;
   const int eq_before = block_exclusive_scan256(eq, warp_tot, tot);
@@ -287,12 +326,18 @@ decode_topk_kernel(const float* __restrict__ ws_scores, const int32_t* __restric
   take_eq = take_eq < 0 ? 0 : (take_eq > eq ? eq : take_eq);
   const int pos0 = block_exclusive_scan256(gt + take_eq, warp_tot, tot);
   int pos = pos0, eq_seen = 0;
-  for (int64_t c = s0; c < s1; ++c) {
-    const float s = sc[c];
-    const uint32_t key = order_key(s);
-    bool take = key > prefix;
-    if (key == prefix) take = eq_seen++ < take_eq;
-    if (take && pos < K) { oid[pos] = int32_t(c); osc[pos] = s; ++pos; }
+  for (int64_t c = s0; c < s1; c += 4) {
+    float s[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[j] = sc[c + j < s1 ? c + j : s1 - 1];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (c + j >= s1) break;
+      const uint32_t key = order_key(s[j]);
+      bool take = key > prefix;
+      if (key == prefix) take = eq_seen++ < take_eq;
+      if (take && pos < K) { oid[pos] = int32_t(c + j); osc[pos] = s[j]; ++pos; }
+    }
   }
 }
 
@@ -301,7 +346,7 @@ decode_topk_kernel(const float* __restrict__ ws_scores, const int32_t* __restric
 // in registers, so the scores are read once instead of once per pass.
 template <int IT>
 __global__ void __launch_bounds__(256)
-decode_topk_reg_kernel(const float* __restrict__ ws_scores, const int32_t* __restrict__ seqlens, int64_t cap,
+decode_topk_reg_kernel(Late<float> ws_scores, const int32_t* __restrict__ seqlens, int64_t cap,
                        int64_t nc, int Hq, int K, int32_t* __restrict__ sel_ids, float* __restrict__ sel_scores,
                        int wm1) {
   __shared__ uint32_t hist[256];
@@ -312,7 +357,7 @@ decode_topk_reg_kernel(const float* __restrict__ ws_scores, const int32_t* __res
   const int row = blockIdx.x, b = row / Hq, tid = threadIdx.x;
   int64_t n = decode_own_chunk(seqlens, b, cap) - wm1;   // candidates
   if (n < 0) n = 0;
-  const float* sc = ws_scores + int64_t(row) * nc;
+  const Late<float> sc = ws_scores + int64_t(row) * nc;
   int32_t* oid = sel_ids + int64_t(row) * K;
   float* osc = sel_scores + int64_t(row) * K;
   if (n <= K) {
@@ -458,7 +503,7 @@ template <typename T, int D>
 __global__ void __launch_bounds__(128, sizeof(T) == 2 ? 8 : 6)
 decode_partial_union_kernel(const T* __restrict__ q, const T* __restrict__ kc, const T* __restrict__ vc,
                             const int32_t* __restrict__ seqlens, int64_t cap, int Hq, int G, int Hkv, int K,
-                            float tau, const int32_t* __restrict__ sel_ids, const float* __restrict__ sel_scores,
+                            float tau, Late<int32_t> sel_ids, Late<float> sel_scores,
                             float* __restrict__ part_u, float* __restrict__ part_o, PagedKv pk, int wm1) {
   using U = DecUnion<T, D>;
   constexpr int EL = D / 32;                 // output dims per lane
@@ -712,10 +757,9 @@ constexpr int kCombBlock = 24;
 
 template <typename T, int D>
 __global__ void __launch_bounds__(D)
-decode_combine_kernel(const float* __restrict__ part_u, const float* __restrict__ part_o,
+decode_combine_kernel(Late<float> part_u, Late<float> part_o,
                       const int32_t* __restrict__ seqlens, int64_t cap, int Hq, int K,
-                      const int32_t* __restrict__ sel_ids, const float* __restrict__ sel_scores,
-                      T* __restrict__ o, int32_t* __restrict__ ids_out, float* __restrict__ scores_out,
+                      Late<int32_t> sel_ids, Late<float> sel_scores, T* __restrict__ o, int32_t* __restrict__ ids_out, float* __restrict__ scores_out,
                       int64_t n_rows, int wm1) {
   pdl_wait();      // the partial outputs
   const int t = threadIdx.x;
@@ -723,15 +767,14 @@ decode_combine_kernel(const float* __restrict__ part_u, const float* __restrict_
   const int b = int(row / Hq);
   const bool valid = decode_own_chunk(seqlens, b, cap) >= 0;
   const int PS = K + wm1 + 1;
-  const float* pu = part_u + row * PS;
-  const float* po = part_o + row * PS * D + t;
+  const Late<float> pu = part_u + row * PS, po = part_o + row * PS * D + t;
   float M = -INFINITY, Z = 0.f, acc = 0.f;
   for (int s0 = 0; s0 < PS; s0 += kCombBlock) {
     float u[kCombBlock], x[kCombBlock];
 #pragma unroll
     for (int e = 0; e < kCombBlock; ++e) {
       const bool in = s0 + e < PS;
-      u[e] = in ? __ldg(pu + s0 + e) : -INFINITY;
+      u[e] = in ? pu[s0 + e] : -INFINITY;
       x[e] = in ? po[int64_t(s0 + e) * D] : 0.f;
     }
     float m = M;

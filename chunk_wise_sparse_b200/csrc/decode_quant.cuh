@@ -13,20 +13,6 @@
 
 namespace hils {
 
-// Loads of what the kernel before wrote, after pdl_wait(): the compiler may
-// move a plain load of constant memory (const __restrict__, __ldg) above the
-// wait, because it takes that memory for unchanging while the kernel runs.
-__device__ __forceinline__ float load_late(const float* p) {
-  float v;
-  asm volatile("ld.global.cg.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
-  return v;
-}
-__device__ __forceinline__ float4 load_late4(const float* p) {
-  float4 v;
-  asm volatile("ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p) : "memory");
-  return v;
-}
-
 // ---------------------------------------------------------------- Q1
 // One warp scores 16 chunks against the query heads of a kv head, eight heads
 // per matrix instruction (rows: chunks, columns: heads).  The order of the
@@ -165,7 +151,7 @@ __device__ __forceinline__ uint32_t warp_kth_key(const uint32_t (&v)[R], int K) 
 // A kept chunk's page is looked up here, by the thread that keeps it.
 template <int IT, int NT>
 __global__ void __launch_bounds__(NT)
-quant_topk_kernel(const float* ws_scores, const int32_t* __restrict__ seqlens, int64_t cap, int64_t nc,
+quant_topk_kernel(Late<float> ws_scores, const int32_t* __restrict__ seqlens, int64_t cap, int64_t nc,
                   int Hq, int K, const int32_t* __restrict__ table, int64_t n_pages, Kept* __restrict__ kept,
                   int32_t* __restrict__ ids_out, float* __restrict__ scores_out, int wm1) {
   constexpr int NW = NT / 32;
@@ -179,7 +165,7 @@ quant_topk_kernel(const float* ws_scores, const int32_t* __restrict__ seqlens, i
   const int64_t b = row / Hq, own = decode_own_chunk(seqlens, int(b), cap);
   int64_t n = own < 0 ? 0 : own - wm1;   // candidates
   if (n < 0) n = 0;
-  const float* sc = ws_scores + int64_t(row) * nc;
+  const Late<float> sc = ws_scores + int64_t(row) * nc;
   const int64_t at = int64_t(row) * K;
   auto put = [&](int slot, int32_t id, float s) {
     if (ids_out) ids_out[at + slot] = id;
@@ -195,7 +181,7 @@ quant_topk_kernel(const float* ws_scores, const int32_t* __restrict__ seqlens, i
     kept[at + slot] = Kept{id, page, s, 0};
   };
   if (n <= K) {
-    for (int t = tid; t < K; t += NT) put(t, t < n ? t : -1, t < n ? load_late(sc + t) : -INFINITY);
+    for (int t = tid; t < K; t += NT) put(t, t < n ? t : -1, t < n ? sc[t] : -INFINITY);
     return;
   }
   const int64_t seg = IT > 0 ? ((n + NT - 1) / NT + 3) / 4 * 4 : (n + NT - 1) / NT;
@@ -209,12 +195,12 @@ quant_topk_kernel(const float* ws_scores, const int32_t* __restrict__ seqlens, i
     for (int e = 0; e < IT; e += 4) {
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       if (vec && e + 4 <= cnt) {
-        v = load_late4(sc + s0 + e);
+        v = sc.wide<float4>(s0 + e);
       } else {
-        if (e < cnt) v.x = load_late(sc + s0 + e);
-        if (e + 1 < cnt) v.y = load_late(sc + s0 + e + 1);
-        if (e + 2 < cnt) v.z = load_late(sc + s0 + e + 2);
-        if (e + 3 < cnt) v.w = load_late(sc + s0 + e + 3);
+        if (e < cnt) v.x = sc[s0 + e];
+        if (e + 1 < cnt) v.y = sc[s0 + e + 1];
+        if (e + 2 < cnt) v.z = sc[s0 + e + 2];
+        if (e + 3 < cnt) v.w = sc[s0 + e + 3];
       }
       // key 0, which no score has, marks the places behind the end
       key[e] = e < cnt ? score_key(v.x) : 0u;
@@ -223,7 +209,7 @@ quant_topk_kernel(const float* ws_scores, const int32_t* __restrict__ seqlens, i
       key[e + 3] = e + 3 < cnt ? score_key(v.w) : 0u;
     }
   }
-  auto key_at = [&](int64_t e) { return score_key(load_late(sc + s0 + e)); };
+  auto key_at = [&](int64_t e) { return score_key(sc[s0 + e]); };
   auto for_keys = [&](auto f) {   // over this thread's keys (and, with IT > 0, zeros behind them)
     if constexpr (IT > 0) {
 #pragma unroll
@@ -396,7 +382,7 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kQdWarps * 32, 2)
 quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, const uint8_t* __restrict__ vpg,
                     const int32_t* __restrict__ table, int64_t n_pages, const int32_t* __restrict__ seqlens,
-                    int64_t cap, int Hq, int G, int Hkv, int K, float tau, const Kept* kept,
+                    int64_t cap, int Hq, int G, int Hkv, int K, float tau, Late<Kept> kept,
                     T* __restrict__ o, int n_oct, int wm1) {
   using A = QuantAttend<D>;
   using P = QuantPage<D>;
@@ -518,8 +504,8 @@ quant_attend_kernel(const T* __restrict__ q, const uint8_t* __restrict__ kpg, co
     const int pair = tid + e * TH;
     mine[e] = make_int4(-1, -1, 0, 0);
     if (pair < n_sel) {
-      const float4 k = load_late4(reinterpret_cast<const float*>(kept + row0 * K + pair));
-      mine[e] = make_int4(__float_as_int(k.x), __float_as_int(k.y), __float_as_int(k.z), 0);
+      const Kept k = kept[row0 * K + pair];
+      mine[e] = make_int4(k.id, k.page, __float_as_int(k.score), 0);
       ids[pair] = uint32_t(mine[e].x);
       scs[pair] = __int_as_float(mine[e].z) * kLog2e;
     }

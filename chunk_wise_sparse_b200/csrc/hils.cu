@@ -570,13 +570,13 @@ int launch_decode(const hils_dims* d, const void* q, const void* kc, const void*
   const dim3 g2(static_cast<unsigned>(rows));
   cudaError_t e;
   if (nc <= 256 * 16)
-    e = launch_pdl(decode_topk_reg_kernel<16>, g2, 256, 0, st, ws.scores, seqlens, d->seqlen, nc, d->heads_q, K,
+    e = launch_pdl(decode_topk_reg_kernel<16>, g2, 256, 0, st, Late<float>{ws.scores}, seqlens, d->seqlen, nc, d->heads_q, K,
                    ws.sel_ids, ws.sel_scores, wm1);
   else if (nc <= 256 * 32)
-    e = launch_pdl(decode_topk_reg_kernel<32>, g2, 256, 0, st, ws.scores, seqlens, d->seqlen, nc, d->heads_q, K,
+    e = launch_pdl(decode_topk_reg_kernel<32>, g2, 256, 0, st, Late<float>{ws.scores}, seqlens, d->seqlen, nc, d->heads_q, K,
                    ws.sel_ids, ws.sel_scores, wm1);
   else
-    e = launch_pdl(decode_topk_kernel, g2, 256, 0, st, ws.scores, seqlens, d->seqlen, nc, d->heads_q, K, ws.sel_ids,
+    e = launch_pdl(decode_topk_kernel, g2, 256, 0, st, Late<float>{ws.scores}, seqlens, d->seqlen, nc, d->heads_q, K, ws.sel_ids,
                    ws.sel_scores, wm1);
   if (e != cudaSuccess) return HILS_ERR_CUDA;
   const size_t smem3 = DecUnion<T, D>::smem(G, K);
@@ -585,13 +585,11 @@ int launch_decode(const hils_dims* d, const void* q, const void* kc, const void*
   const dim3 g3(unsigned(G * K + wm1 + 1), unsigned(d->batch * d->heads_kv));
   e = launch_pdl(k3, g3, 128, smem3, st, static_cast<const T*>(q), static_cast<const T*>(kc),
                  static_cast<const T*>(vc), seqlens, d->seqlen, d->heads_q, G, d->heads_kv, K, tau,
-                 static_cast<const int32_t*>(ws.sel_ids), static_cast<const float*>(ws.sel_scores), ws.part_u,
-                 ws.part_o, pk, wm1);
+                 Late<int32_t>{ws.sel_ids}, Late<float>{ws.sel_scores}, ws.part_u, ws.part_o, pk, wm1);
   if (e != cudaSuccess) return HILS_ERR_CUDA;
   e = launch_pdl(decode_combine_kernel<T, D>, dim3(unsigned(rows)), D, 0, st,
-                 static_cast<const float*>(ws.part_u), static_cast<const float*>(ws.part_o), seqlens, d->seqlen,
-                 d->heads_q, K, static_cast<const int32_t*>(ws.sel_ids), static_cast<const float*>(ws.sel_scores),
-                 static_cast<T*>(o), ids_out, scores_out, rows, wm1);
+                 Late<float>{ws.part_u}, Late<float>{ws.part_o}, seqlens, d->seqlen, d->heads_q, K,
+                 Late<int32_t>{ws.sel_ids}, Late<float>{ws.sel_scores}, static_cast<T*>(o), ids_out, scores_out, rows, wm1);
   if (e != cudaSuccess) return HILS_ERR_CUDA;
   return launched(4);
 }
@@ -1023,7 +1021,7 @@ int launch_decode_quant(const hils_dims* d, const void* q, const void* q_score, 
   const auto* kpool = static_cast<const uint8_t*>(kpg);
   const auto* vpool = static_cast<const uint8_t*>(vpg);
   auto topk = [&](auto* fn, int threads) {
-    return launch_pdl(fn, dim3(unsigned(rows)), threads, 0, st, static_cast<const float*>(ws.scores), seqlens, d->seqlen,
+    return launch_pdl(fn, dim3(unsigned(rows)), threads, 0, st, Late<float>{ws.scores}, seqlens, d->seqlen,
                       nc, int(d->heads_q), K, table, n_pages, ws.kept, ids_out, scores_out, wm1);
   };
   cudaError_t e = nc <= 256 * 8     ? topk(quant_topk_kernel<8, 256>, 256)
@@ -1054,7 +1052,7 @@ int launch_decode_quant(const hils_dims* d, const void* q, const void* q_score, 
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   e = cudaLaunchKernelEx(&cfg, k3, static_cast<const T*>(q), kpool, vpool, table, n_pages, seqlens, d->seqlen,
-                         int(d->heads_q), G, int(d->heads_kv), K, tau, static_cast<const Kept*>(ws.kept),
+                         int(d->heads_q), G, int(d->heads_kv), K, tau, Late<Kept>{ws.kept},
                          static_cast<T*>(o), n_oct, wm1);
   if (e != cudaSuccess) return HILS_ERR_CUDA;
   return launched(3);
