@@ -842,19 +842,19 @@ static int check_tokens(const hils_dims* d, const hils_tokens* tk, TokenBatch* t
 }
 
 // Rows [T, heads, d]: 16-byte aligned, strides in elements of whole 16-byte
-// pieces; those of an output must not make two rows overlap.
-static bool rows_ok(const hils_rows* r, const hils_dims* d, int64_t T, int64_t heads, bool output) {
+// pieces; those of an output must not make two rows overlap.  A stride between
+// tokens (heads) is looked at where there are several.
+static bool take_rows(const hils_rows* r, const hils_dims* d, int64_t T, int64_t heads, bool output, RowsView* view) {
   if (r == nullptr || !ptr_ok(r->data)) return false;
-  const int64_t per16 = d->dtype == HILS_BF16 ? 8 : 4, D = d->head_dim, ts = r->token_stride, hs = r->head_stride;
+  const int64_t per16 = d->dtype == HILS_BF16 ? 8 : 4, D = d->head_dim;
+  const int64_t ts = T > 1 ? r->token_stride : 0, hs = heads > 1 ? r->head_stride : 0;
+  *view = RowsView{r->data, ts, hs};
   if (ts < 0 || hs < 0 || ts % per16 != 0 || hs % per16 != 0) return false;
   // every offset fits 62 bits
   if (__int128(T - 1) * ts + __int128(heads - 1) * hs + D >= (__int128(1) << 62)) return false;
   if (!output) return true;
   if ((T > 1 && ts < D) || (heads > 1 && hs < D)) return false;
   return T == 1 || heads == 1 || ts >= (heads - 1) * hs + D || hs >= (T - 1) * ts + D;
-}
-static RowsView rows_view(const hils_rows* r) {
-  return r == nullptr ? RowsView{nullptr, 0, 0} : RowsView{r->data, r->token_stride, r->head_stride};
 }
 
 }  // extern "C"
@@ -906,15 +906,13 @@ int append_entry(const hils_dims* d, const hils_tokens* tk, const hils_rotary* r
   if ((q == nullptr) != (q_out == nullptr)) return HILS_ERR_INVALID_ARGUMENT;
   if (p.tb.n_tokens == 0) return HILS_OK;
   const int64_t T = p.tb.n_tokens;
-  if (q != nullptr && (!rows_ok(q, d, T, d->heads_q, false) || !rows_ok(q_out, d, T, d->heads_q, true)))
+  p.q = p.q_out = RowsView{nullptr, 0, 0};
+  if (q != nullptr &&
+      (!take_rows(q, d, T, d->heads_q, false, &p.q) || !take_rows(q_out, d, T, d->heads_q, true, &p.q_out)))
     return HILS_ERR_INVALID_ARGUMENT;
-  if (!rows_ok(k, d, T, d->heads_kv, false) || !rows_ok(v, d, T, d->heads_kv, false) || !ptr_ok(k_pages) ||
-      !ptr_ok(v_pages) || !ptr_ok(page_table))
+  if (!take_rows(k, d, T, d->heads_kv, false, &p.k) || !take_rows(v, d, T, d->heads_kv, false, &p.v) ||
+      !ptr_ok(k_pages) || !ptr_ok(v_pages) || !ptr_ok(page_table))
     return HILS_ERR_INVALID_ARGUMENT;
-  p.q = rows_view(q);
-  p.q_out = rows_view(q_out);
-  p.k = rows_view(k);
-  p.v = rows_view(v);
   p.k_pages = k_pages;
   p.v_pages = v_pages;
   p.table = page_table;
@@ -1088,11 +1086,10 @@ int hils_kv_read_quant(const hils_dims* d, const hils_tokens* tokens, const void
   if (n_pages < 1 || (k == nullptr && v == nullptr)) return HILS_ERR_INVALID_ARGUMENT;
   const int64_t T = p.tb.n_tokens;
   if (T == 0) return HILS_OK;
-  if ((k != nullptr && (!rows_ok(k, d, T, d->heads_kv, true) || !ptr_ok(k_pages))) ||
-      (v != nullptr && (!rows_ok(v, d, T, d->heads_kv, true) || !ptr_ok(v_pages))) || !ptr_ok(page_table))
+  p.k = p.v = RowsView{nullptr, 0, 0};
+  if ((k != nullptr && (!take_rows(k, d, T, d->heads_kv, true, &p.k) || !ptr_ok(k_pages))) ||
+      (v != nullptr && (!take_rows(v, d, T, d->heads_kv, true, &p.v) || !ptr_ok(v_pages))) || !ptr_ok(page_table))
     return HILS_ERR_INVALID_ARGUMENT;
-  p.k = rows_view(k);
-  p.v = rows_view(v);
   p.k_pages = static_cast<const uint8_t*>(k_pages);
   p.v_pages = static_cast<const uint8_t*>(v_pages);
   p.table = page_table;

@@ -346,7 +346,8 @@ typedef struct hils_tokens {
 
 /* Rows [T, heads, d] of `dtype`, d innermost and dense, with any token and
  * head stride in elements (a view of a fused projection, or head-major).
- * data 16-byte aligned, strides non-negative multiples of 16 bytes; the rows
+ * data 16-byte aligned, strides non-negative multiples of 16 bytes (the
+ * stride of a single token, or of a single head, is not looked at); the rows
  * of an output must not overlap (HILS_ERR_INVALID_ARGUMENT). */
 typedef struct hils_rows {
   void* data;
