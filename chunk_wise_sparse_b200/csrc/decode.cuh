@@ -52,17 +52,19 @@ template <typename T> struct Late {
   static_assert(sizeof(T) == 4 || sizeof(T) == 16, "one 32-bit or 128-bit load");
   const T* p;
   __device__ __forceinline__ T operator[](int64_t i) const {
-    union { uint32_t w[sizeof(T) / 4]; T v; } x;
+    union { uint32_t w[4]; T v; } x;
     if constexpr (sizeof(T) == 4)
       asm volatile("ld.global.b32 %0, [%1];" : "=r"(x.w[0]) : "l"(p + i));
     else
       asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(x.w[0]), "=r"(x.w[1 % (sizeof(T) / 4)]), "=r"(x.w[2 % (sizeof(T) / 4)]), "=r"(x.w[3 % (sizeof(T) / 4)])
+                   : "=r"(x.w[0]), "=r"(x.w[1]), "=r"(x.w[2]), "=r"(x.w[3])
                    : "l"(p + i));
     return x.v;
   }
   // elements i .. as one wider value (aligned to it)
-  template <typename V> __device__ __forceinline__ V wide(int64_t i) const { return Late<V>{reinterpret_cast<const V*>(p + i)}[0]; }
+  template <typename V> __device__ __forceinline__ V wide(int64_t i) const {
+    return Late<V>{reinterpret_cast<const V*>(p + i)}[0];
+  }
   __device__ __forceinline__ Late operator+(int64_t i) const { return Late{p + i}; }
 };
 
@@ -759,7 +761,8 @@ template <typename T, int D>
 __global__ void __launch_bounds__(D)
 decode_combine_kernel(Late<float> part_u, Late<float> part_o,
                       const int32_t* __restrict__ seqlens, int64_t cap, int Hq, int K,
-                      Late<int32_t> sel_ids, Late<float> sel_scores, T* __restrict__ o, int32_t* __restrict__ ids_out, float* __restrict__ scores_out,
+                      Late<int32_t> sel_ids, Late<float> sel_scores, T* __restrict__ o,
+                      int32_t* __restrict__ ids_out, float* __restrict__ scores_out,
                       int64_t n_rows, int wm1) {
   pdl_wait();      // the partial outputs
   const int t = threadIdx.x;

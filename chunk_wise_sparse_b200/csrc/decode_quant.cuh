@@ -339,17 +339,19 @@ quant_topk_kernel(Late<float> ws_scores, const int32_t* __restrict__ seqlens, in
 // values (24 bits), so that the products are fp32's.
 // Running maximum, sum and outputs stay in registers over a warp's chunks;
 // warps merge in shared memory, CTAs through distributed shared memory.
-// Bound by instruction issue inside a chunk (about 1600) and by what surrounds
-// it: the first chunks of all warps arrive together (3.8 us), and a warp has
-// one chunk more or less than another.  8 sequences of 128K, 64 chunks per kv
-// head: 19 us of the step's 37.5 (its 42 MB would take 6.4).  Two CTAs of six
-// warps per SM, for 168 registers a thread: of eight (128 registers, spills)
-// 43 us for the step, seven 39.6, five 40.3, four 38.8, three of four 39.3, one
-// of eight 41.5.  Also measured, for the step at the time: a warp per (head,
-// slot) on CUDA cores 118 us; four warps per chunk instead of one 55 against 45
-// (each repeats the softmax and the fusion: 2900 instructions per chunk); codes
-// widened to bf16 16 + code 47; slots in place of the list of distinct chunks
-// 63 against 47.
+// Bound by latency: three warps per scheduler wait for chains of their own
+// (about 1430 instructions per chunk with their fixed latencies and shared
+// memory, then the next chunk's copies), and at the end for the warps that have
+// one chunk more; the first chunks of all warps arrive together (3.8 us).  37 %
+// of issue slots are busy with 64 chunks per kv head, 48 % with 190.  8
+// sequences of 128K, 64 chunks per kv head: 19 us of the step's 37.4 (its 41 MB
+// would take 6.3).  Two CTAs of six warps per SM, for 168 registers a thread:
+// of eight (128 registers, spills) 43 us for the step, seven 39.6, five 40.3,
+// four 38.8, three of four 39.3, one of eight 41.5.  Also measured, for the step
+// at the time: a warp per (head, slot) on CUDA cores 118 us; four warps per
+// chunk instead of one 55 against 45 (each repeats the softmax and the fusion:
+// 2900 instructions per chunk); codes widened to bf16 16 + code 47; slots in
+// place of the list of distinct chunks 63 against 47.
 constexpr int kQdWarps = 6;
 
 // The power of two (its bits) that puts the largest step, given by its bits, in
@@ -367,9 +369,10 @@ template <int D> struct QuantAttend {
   static constexpr int RS = D + 4;                            // floats per merged row: 16-byte stores of four rows apart
   static constexpr int MERGE = 8 * RS * 4 + 8 * 2 * 4;        // per warp: 8 rows, then (maximum, sum) of 8 heads
   static constexpr int STAGE = 2 * BLOCK > MERGE ? 2 * BLOCK : (MERGE + 15) / 16 * 16;
-  // a CTA's sums of one head: D values, maximum, sum; up to 15 arrive at the CTA
-  // that finishes some of eight heads in a cluster of up to eight
-  static constexpr int PART = D + 4, INBOX = 15 * PART;
+  // a CTA's sums of one head: D values, maximum, sum.  A CTA that finishes some
+  // of eight heads in a cluster of CL keeps ceil(8 / CL) rows of CL, 14 at most
+  // (CL = 7)
+  static constexpr int PART = D + 4, INBOX = 14 * PART;
   static constexpr int LISTS = 8 * kMaxTopK;                  // kept (head, slot) pairs of a cluster, at most
   static constexpr int ITEMS = LISTS + 16;                    // distinct chunks and window chunks
   // staging, the CTAs' sums of the heads this one finishes, scores of the pairs,
