@@ -650,7 +650,9 @@ def kv_append(k_pages, v_pages, page_table, k, v, seqlens, cu_tokens=None, rotar
               stream=None):
     """Append the packed new keys and values k, v [T,Hkv,d] to a chunk-paged cache (bf16 / fp32 or 4-bit pages),
     rotating keys, and queries q [T,Hq,d], by their positions.  k, v, q may be views with any token and head stride.
-    Returns the rotated queries (q_out, or a new [T,Hq,d]; None without q)."""
+    Returns the rotated queries (q_out, or a new [T,Hq,d]; None without q).  Rows of tokens that are skipped (behind
+    the last sequence, or of a sequence that does not fit) are not written: q_out keeps what it held there, a new
+    tensor holds anything."""
     dtype = k.dtype
     quant, n_pages, Hkv, d = _page_kind(k_pages, v_pages, dtype)
     B, nc = _batch(page_table, seqlens, cu_tokens)
@@ -675,7 +677,8 @@ def kv_append(k_pages, v_pages, page_table, k, v, seqlens, cu_tokens=None, rotar
 def kv_read(k_pages, v_pages, page_table, seqlens, n_tokens, dtype, cu_tokens=None, k_out=None, v_out=None,
             stream=None):
     """The last n_b cached rows of every sequence of a 4-bit cache as (k, v) [T,Hkv,d] of `dtype`; k_out, v_out may
-    have any token and head stride, e.g. cache[0].transpose(0, 1) of a contiguous cache [1,Hkv,N,d]."""
+    have any token and head stride, e.g. cache[0].transpose(0, 1) of a contiguous cache [1,Hkv,N,d].  Rows of tokens
+    that are skipped are not written: k_out and v_out keep what they held there, new tensors hold anything."""
     quant, n_pages, Hkv, d = _page_kind(k_pages, v_pages, dtype)
     if not quant:
         raise ValueError("kv_read reads 4-bit pages")
@@ -711,8 +714,8 @@ def landmark_summary_append(k_pages, page_table, lq, seqlens, n_tokens, summ: Su
     _need(lq, "lq", lq.dtype, (B, Hkv, nc, d))
     _need_summary(summ, B, Hkv, nc, d, lq.dtype)
     call = hils_landmark_summary_quant if quant else hils_landmark_summary_append
-    call(_dims_of(B, Hkv, Hkv, d, nc, 1, lq.dtype, 0), seqlens, n_tokens, cu_tokens, k_pages, page_table, n_pages, lq, summ.kprime, summ.bprime,
-         summ.kprime_mma, stream)
+    call(_dims_of(B, Hkv, Hkv, d, nc, 1, lq.dtype, 0), seqlens, n_tokens, cu_tokens, k_pages, page_table, n_pages, lq,
+         summ.kprime, summ.bprime, summ.kprime_mma, stream)
     return summ
 
 

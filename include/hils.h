@@ -418,9 +418,11 @@ size_t hils_quant_page_bytes(const hils_dims* dims);
 
 /*
  * Read rows of a 4-bit cache back: the positions that `tokens` describes (the
- * last n_b of every sequence; cu_tokens as differences of seqlens reads whole
- * sequences), as values m + s * code rounded to dtype -- a cached prefix for
- * hils_attn_prefill, or a sequence moved to an unquantised cache.
+ * last n_b of every sequence; with the running sums of seqlens as cu_tokens,
+ * whole sequences), as values m + s * code rounded to dtype -- a sequence moved
+ * to an unquantised cache, or the keys and values of a call on a contiguous one
+ * (hils_attn_prefill then wants the queries of every position, not of the new
+ * ones alone).
  *   k, v   [T, Hkv, d] out (either may be NULL)
  * Tokens that cannot be placed, or whose page is outside the pool, are
  * recorded as HILS_ERR_DEVICE_BOUNDS and their rows left as they were.
